@@ -1,7 +1,7 @@
 """scaled_quantization_amd -- scaled FP8 quantization for an MLP down-projection on MI355X.
 
 A thin ctypes binding over ``libfp8dp.so`` (C ABI declared in
-``include/fp8dp.h``).  Every step of the path runs in the library's HIP
+``include/fp8dp.h`` and ``include/fp8dp_block.h``).  Every step of the path runs in the library's HIP
 kernels; this module only marshals torch device tensors into pointers, sizes
 and the current HIP stream, and turns nonzero return codes into exceptions.
 It raises if the library has not been built; there is no CPU fallback.
@@ -13,6 +13,10 @@ Entry points (same names as the C ABI):
     quantize_mx, quantize_mx_transposed, fp8_gemm_mx, fp8_gemm_mx_splitk, and the
     comparison / diagnostic calls fp8dp_bench_*, fp8dp_convert_f32, fp8dp_scale_rule,
     fp8dp_set_grid_limit, fp8dp_set_codec.
+Operators around the MLP (include/fp8dp_block.h):
+    layer_norm, layer_norm_backward, dropout_add, dropout_add_layer_norm,
+    quantize_int8, layer_norm_quantize_int8, int8_gemm, int8_linear,
+    int8_linear_workspace.
 """
 from __future__ import annotations
 
@@ -31,6 +35,8 @@ ACCUM_MFMA_FP8, ACCUM_EXACT = 0, 1
 MAX_HIST = 16
 ACC_SLOTS = 64
 STATE_BYTES = 4288
+NORM_PARTS = 1024        # layer_norm_backward's workspace: 2 * min(rows, NORM_PARTS) * cols floats
+INT8_MAX_K = 131071
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp8dp.so")
@@ -72,6 +78,21 @@ _SIGS = {
                     ctypes.c_int),
     "gemm_bf16_quantize_fused": ([_vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp,
                                   _vp], ctypes.c_int),
+    "layer_norm": ([_vp, _vp, _vp, _i64, _i64, _i32, _i32, _f32, _vp, _vp, _vp, _vp],
+                   ctypes.c_int),
+    "dropout_add": ([_vp, _vp, _i64, _i64, _i32, _f32, _vp, _vp, _vp], ctypes.c_int),
+    "dropout_add_layer_norm": ([_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _f32, _vp, _f32, _vp,
+                                _vp, _vp, _vp, _vp], ctypes.c_int),
+    "layer_norm_backward": ([_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _f32, _vp,
+                             _vp, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "quantize_int8": ([_vp, _i64, _i64, _i32, _vp, _vp, _vp], ctypes.c_int),
+    "layer_norm_quantize_int8": ([_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _f32, _vp, _vp,
+                                  _vp, _vp], ctypes.c_int),
+    "int8_gemm": ([_vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _i64, _vp],
+                  ctypes.c_int),
+    "int8_linear_workspace": ([_i64, _i64], _i64),
+    "int8_linear": ([_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _i64, _vp],
+                    ctypes.c_int),
     "fp8dp_last_error": ([], ctypes.c_char_p),
     "fp8dp_bench_act_bf16": ([_vp, _i64, _i32, _vp, _vp], ctypes.c_int),
     "fp8dp_bench_amax": ([_vp, _i64, _vp, _vp], ctypes.c_int),
@@ -531,6 +552,212 @@ def gemm_bf16_quantize_fused(x: torch.Tensor, w: torch.Tensor, act: int = ACT_RE
     _check(lib().gemm_bf16_quantize_fused(_p(x), _p(w), M, N, K, act, fmt, _state_ptr(st),
                                           _p(h_out), _p(bf16_out), _p(fp8_out), _stream(stream)),
            "gemm_bf16_quantize_fused")
+
+
+# --------------------------------------------------------------------------- around the MLP
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _dtype(t: torch.Tensor, what: str) -> int:
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise Fp8dpError(f"{what}: expected bfloat16, float16 or float32, got {t.dtype}")
+    return d
+
+
+def _like(t, x: torch.Tensor, what: str) -> None:
+    """Refuse a tensor that is not of x's shape and type (None passes)."""
+    if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+        raise Fp8dpError(f"{what}: expected {x.dtype} {tuple(x.shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+
+
+def _floats(t, n: int, what: str) -> None:
+    """Refuse a tensor that does not hold exactly n float32 values (None passes)."""
+    if t is not None and (t.dtype != torch.float32 or t.numel() != n):
+        raise Fp8dpError(f"{what}: expected {n} float32 values, got {t.dtype} {tuple(t.shape)}")
+
+
+def _params(ts, dtype: torch.dtype, n: int, what: str) -> int:
+    """Type code of parameter vectors of n values: all of type `dtype`, or all float32."""
+    got = None
+    for t in ts:
+        if t is None:
+            continue
+        if t.numel() != n or t.dtype not in (dtype, torch.float32) or got not in (None, t.dtype):
+            raise Fp8dpError(f"{what}: expected {n} values each, all {dtype} or all "
+                             f"float32, got {t.dtype} {tuple(t.shape)}")
+        got = t.dtype
+    return _DTYPES[got or dtype]
+
+
+def _rng(rng, what: str) -> None:
+    """Refuse random number words other than [seed, offset], two 64-bit integers."""
+    if rng is not None and (rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2):
+        raise Fp8dpError(f"{what}: rng must be two 64-bit integers, seed and offset, got "
+                         f"{rng.dtype} {tuple(rng.shape)}")
+
+
+def _last(x: torch.Tensor, what: str) -> tuple:
+    """(rows, cols) with cols the last dimension."""
+    if x.dim() == 0:
+        raise Fp8dpError(f"{what}: expected at least one dimension")
+    cols = x.shape[-1]
+    return (x.numel() // cols if cols else 0), cols
+
+
+def layer_norm(x: torch.Tensor, weight, bias, eps: float, y: torch.Tensor, mean=None, rstd=None,
+               stream=None) -> None:
+    """y = (x - mean) rstd weight + bias over the last dimension; bfloat16, float16 or
+    float32, weight and bias of the same type or float32 (None: ones, zeros);
+    mean, rstd: float32, one value per row, for the backward pass."""
+    dt = _dtype(x, "layer_norm: x")
+    rows, cols = _last(x, "layer_norm: x")
+    _like(y, x, "layer_norm: y")
+    wt = _params((weight, bias), x.dtype, cols, "layer_norm: weight, bias")
+    _floats(mean, rows, "layer_norm: mean")
+    _floats(rstd, rows, "layer_norm: rstd")
+    _check(lib().layer_norm(_p(x), _p(weight), _p(bias), rows, cols, dt, wt, eps, _p(y), _p(mean),
+                            _p(rstd), _stream(stream)), "layer_norm")
+
+
+def layer_norm_backward(dy: torch.Tensor, z: torch.Tensor, weight, mean: torch.Tensor,
+                        rstd: torch.Tensor, dz: torch.Tensor, dweight=None, dbias=None,
+                        workspace=None, dz_add=None, p: float = 0.0, rng=None, dx=None,
+                        stream=None) -> None:
+    """Gradients of layer_norm at its input z: dz (plus dz_add, the gradient that
+    passes the norm by), dweight and dbias (float32; with them workspace, float32
+    of 2 * min(rows, NORM_PARTS) * cols values), and dx, dz through the mask of
+    dropout_add_layer_norm's p and rng."""
+    dt = _dtype(z, "layer_norm_backward: z")
+    rows, cols = _last(z, "layer_norm_backward: z")
+    for t, name in ((dy, "dy"), (dz, "dz"), (dz_add, "dz_add"), (dx, "dx")):
+        _like(t, z, f"layer_norm_backward: {name}")
+    wt = _params((weight,), z.dtype, cols, "layer_norm_backward: weight")
+    _floats(mean, rows, "layer_norm_backward: mean")
+    _floats(rstd, rows, "layer_norm_backward: rstd")
+    _floats(dweight, cols, "layer_norm_backward: dweight")
+    _floats(dbias, cols, "layer_norm_backward: dbias")
+    _rng(rng, "layer_norm_backward")
+    if dweight is not None and workspace is not None and (
+            workspace.dtype != torch.float32
+            or workspace.numel() < 2 * min(rows, NORM_PARTS) * cols):
+        raise Fp8dpError("layer_norm_backward: workspace needs 2 * min(rows, "
+                         f"{NORM_PARTS}) * cols = {2 * min(rows, NORM_PARTS) * cols} float32")
+    _check(lib().layer_norm_backward(_p(dy), _p(z), _p(weight), _p(mean), _p(rstd), _p(dz_add),
+                                     rows, cols, dt, wt, p, _p(rng), _p(dz), _p(dx), _p(dweight),
+                                     _p(dbias), _p(workspace), _stream(stream)),
+           "layer_norm_backward")
+
+
+def dropout_add(x: torch.Tensor, residual, p: float, rng, out: torch.Tensor, stream=None) -> None:
+    """out = residual + keep x / (1 - p) (residual None: no sum); rng: [seed, offset], two
+    64-bit integers on the device.  The same call on the gradient is the backward pass."""
+    dt = _dtype(x, "dropout_add: x")
+    rows, cols = _last(x, "dropout_add: x")
+    _like(residual, x, "dropout_add: residual")
+    _like(out, x, "dropout_add: out")
+    _rng(rng, "dropout_add")
+    _check(lib().dropout_add(_p(x), _p(residual), rows, cols, dt, p, _p(rng), _p(out),
+                             _stream(stream)), "dropout_add")
+
+
+def dropout_add_layer_norm(x: torch.Tensor, residual, p: float, rng, weight, bias, eps: float,
+                           z: torch.Tensor, y: torch.Tensor, mean=None, rstd=None,
+                           stream=None) -> None:
+    """z = dropout_add(x, residual) and y = layer_norm(z) in one pass."""
+    dt = _dtype(x, "dropout_add_layer_norm: x")
+    rows, cols = _last(x, "dropout_add_layer_norm: x")
+    for t, name in ((residual, "residual"), (z, "z"), (y, "y")):
+        _like(t, x, f"dropout_add_layer_norm: {name}")
+    wt = _params((weight, bias), x.dtype, cols, "dropout_add_layer_norm: weight, bias")
+    _floats(mean, rows, "dropout_add_layer_norm: mean")
+    _floats(rstd, rows, "dropout_add_layer_norm: rstd")
+    _rng(rng, "dropout_add_layer_norm")
+    _check(lib().dropout_add_layer_norm(_p(x), _p(residual), _p(weight), _p(bias), rows, cols, dt,
+                                        wt, p, _p(rng), eps, _p(z), _p(y), _p(mean), _p(rstd),
+                                        _stream(stream)), "dropout_add_layer_norm")
+
+
+def _int8(t: torch.Tensor, what: str) -> None:
+    if t.dtype != torch.int8:
+        raise Fp8dpError(f"{what}: expected int8 codes, got {t.dtype}")
+
+
+def quantize_int8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None) -> None:
+    """INT8 codes q (x's shape) and one float32 scale per row: x is about q * scale,
+    scale = amax / 127.  Rows are tokens, or the output channels of a weight."""
+    dt = _dtype(x, "quantize_int8: x")
+    rows, cols = _last(x, "quantize_int8: x")
+    _int8(q, "quantize_int8: q")
+    if q.shape != x.shape:
+        raise Fp8dpError("quantize_int8: q must have x's shape")
+    _floats(scale, rows, "quantize_int8: scale")
+    _check(lib().quantize_int8(_p(x), rows, cols, dt, _p(q), _p(scale), _stream(stream)),
+           "quantize_int8")
+
+
+def layer_norm_quantize_int8(x: torch.Tensor, weight, bias, eps: float, q: torch.Tensor,
+                             scale: torch.Tensor, residual=None, z=None, stream=None) -> None:
+    """quantize_int8 of layer_norm(x) in one pass; with residual and z of layer_norm(z),
+    z = x + residual."""
+    dt = _dtype(x, "layer_norm_quantize_int8: x")
+    rows, cols = _last(x, "layer_norm_quantize_int8: x")
+    _like(residual, x, "layer_norm_quantize_int8: residual")
+    _like(z, x, "layer_norm_quantize_int8: z")
+    wt = _params((weight, bias), x.dtype, cols, "layer_norm_quantize_int8: weight, bias")
+    _int8(q, "layer_norm_quantize_int8: q")
+    if q.shape != x.shape:
+        raise Fp8dpError("layer_norm_quantize_int8: q must have x's shape")
+    _floats(scale, rows, "layer_norm_quantize_int8: scale")
+    _check(lib().layer_norm_quantize_int8(_p(x), _p(residual), _p(weight), _p(bias), rows, cols,
+                                          dt, wt, eps, _p(z), _p(q), _p(scale), _stream(stream)),
+           "layer_norm_quantize_int8")
+
+
+def _int8_operands(name: str, a: torch.Tensor, b: torch.Tensor, b_scale, y: torch.Tensor,
+                   bias) -> tuple:
+    """(M, N, K, y's type, bias' type) of a product a [..., K] x b [N, K] -> y [..., N]."""
+    _int8(b, f"{name}: weight")
+    yt = _dtype(y, f"{name}: y")
+    M, K = _last(a, f"{name}: a")
+    if b.dim() != 2 or b.shape[1] != K or y.dim() == 0 or y.shape[:-1] != a.shape[:-1] or \
+            y.shape[-1] != b.shape[0]:
+        raise Fp8dpError(f"{name}: shape mismatch")
+    N = b.shape[0]
+    _floats(b_scale, N, f"{name}: weight scale")
+    return M, N, K, yt, _params((bias,), y.dtype, N, f"{name}: bias")
+
+
+def int8_gemm(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: torch.Tensor,
+              y: torch.Tensor, bias=None, workspace=None, stream=None) -> None:
+    """y [..., N] = (a [..., K] b [N, K]^T) a_scale[row] b_scale[channel] + bias, int8
+    codes summed exactly; y bfloat16, float16 or float32, bias of y's type or float32.
+    workspace (any contiguous tensor, 16-byte aligned) lets K be split where y is small."""
+    _int8(a, "int8_gemm: a")
+    M, N, K, yt, bt = _int8_operands("int8_gemm", a, b, b_scale, y, bias)
+    _floats(a_scale, M, "int8_gemm: a_scale")
+    room = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().int8_gemm(_p(a), _p(b), M, N, K, _p(a_scale), _p(b_scale), _p(bias), yt, bt,
+                           _p(y), _p(workspace), room, _stream(stream)), "int8_gemm")
+
+
+def int8_linear_workspace(M: int, K: int) -> int:
+    """Least workspace of int8_linear in bytes."""
+    return lib().int8_linear_workspace(M, K)
+
+
+def int8_linear(x: torch.Tensor, w8: torch.Tensor, w_scale: torch.Tensor, y: torch.Tensor,
+                workspace: torch.Tensor, bias=None, stream=None) -> None:
+    """y [..., N] = x [..., K] W^T + bias with x cast to INT8 per token (quantize_int8) and W
+    given as codes w8 [N, K] and w_scale [N]; x and y of one type.  workspace: at least
+    int8_linear_workspace(M, K) bytes; up to 16 MiB beyond serve the split of K."""
+    if _dtype(x, "int8_linear: x") != _DTYPES.get(y.dtype):
+        raise Fp8dpError(f"int8_linear: y must be of x's type, {x.dtype}, got {y.dtype}")
+    M, N, K, yt, bt = _int8_operands("int8_linear", x, w8, w_scale, y, bias)
+    _check(lib().int8_linear(_p(x), _p(w8), _p(w_scale), _p(bias), M, N, K, yt, bt, _p(y),
+                             _p(workspace), workspace.numel() * workspace.element_size(),
+                             _stream(stream)), "int8_linear")
 
 
 def fp8dp_bench_act_bf16(h: torch.Tensor, act: int, out: torch.Tensor, stream=None) -> None:

@@ -1,0 +1,357 @@
+// row_core.hpp -- pieces shared by the kernels that work on whole rows (layer
+// norm, dropout, INT8 quantizer): vectors of 8 elements at the alignment of an
+// element, row statistics over a wave or a workgroup, the Philox mask, and
+// the exact INT8 rounding.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "codec.hpp"
+#include "common.hpp"
+#include "fp8dp_block.h"
+
+namespace fp8dp {
+
+// ------------------------------------------------------------------ vectors
+// 16 and 8 bytes at the alignment of one element: gfx950 takes global accesses
+// of any alignment, so rows of odd length need no path of their own.
+typedef unsigned int u32x4_e_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef unsigned int u32x2_b_t __attribute__((ext_vector_type(2), aligned(1)));
+typedef float f32x4_e_t __attribute__((ext_vector_type(4), aligned(4)));
+
+struct bf16_t { uint16_t bits; };
+struct f16_t { uint16_t bits; };
+
+template <typename T> struct Raw8 { u32x4_e_t w; };          // 8 elements as loaded
+template <> struct Raw8<float> { f32x4_e_t lo, hi; };
+
+__device__ __forceinline__ float to_f32(bf16_t x) { return __uint_as_float((uint32_t)x.bits << 16); }
+__device__ __forceinline__ float to_f32(f16_t x) {
+  return (float)__builtin_bit_cast(_Float16, x.bits);
+}
+__device__ __forceinline__ float to_f32(float x) { return x; }
+
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ bf16_t from_f32<bf16_t>(float v) {
+  return {(uint16_t)(pack2_bf16_hw(v, 0.0f) & 0xFFFFu)};
+}
+template <> __device__ __forceinline__ f16_t from_f32<f16_t>(float v) {
+  return {__builtin_bit_cast(uint16_t, (_Float16)v)};
+}
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw8(const T* p) {
+  Raw8<T> r;
+  r.w = *reinterpret_cast<const u32x4_e_t*>(p);
+  return r;
+}
+template <>
+__device__ __forceinline__ Raw8<float> load_raw8<float>(const float* p) {
+  Raw8<float> r;
+  r.lo = *reinterpret_cast<const f32x4_e_t*>(p);
+  r.hi = *reinterpret_cast<const f32x4_e_t*>(p + 4);
+  return r;
+}
+
+__device__ __forceinline__ void widen8f(const Raw8<bf16_t>& r, float v[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(r.w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(r.w[j] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void widen8f(const Raw8<f16_t>& r, float v[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = (float)__builtin_bit_cast(_Float16, (uint16_t)(r.w[j] & 0xFFFFu));
+    v[2 * j + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(r.w[j] >> 16));
+  }
+}
+__device__ __forceinline__ void widen8f(const Raw8<float>& r, float v[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] = r.lo[j];
+    v[j + 4] = r.hi[j];
+  }
+}
+
+__device__ __forceinline__ Raw8<bf16_t> round8(const float v[8], bf16_t) {
+  Raw8<bf16_t> r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r.w[j] = pack2_bf16_hw(v[2 * j], v[2 * j + 1]);
+  return r;
+}
+__device__ __forceinline__ Raw8<f16_t> round8(const float v[8], f16_t) {
+  Raw8<f16_t> r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    r.w[j] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v[2 * j]) |
+             (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v[2 * j + 1]) << 16;
+  return r;
+}
+__device__ __forceinline__ Raw8<float> round8(const float v[8], float) {
+  Raw8<float> r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    r.lo[j] = v[j];
+    r.hi[j] = v[j + 4];
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void store_raw8(T* p, const Raw8<T>& r) {
+  *reinterpret_cast<u32x4_e_t*>(p) = r.w;
+}
+template <>
+__device__ __forceinline__ void store_raw8<float>(float* p, const Raw8<float>& r) {
+  *reinterpret_cast<f32x4_e_t*>(p) = r.lo;
+  *reinterpret_cast<f32x4_e_t*>(p + 4) = r.hi;
+}
+
+// The n elements at p (n >= 8: 8 of them; n <= 0: none), the rest zeros.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int n, float v[8]) {
+  if (n >= 8) {
+    widen8f(load_raw8(p), v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? to_f32(p[j]) : 0.0f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int n, const float v[8]) {
+  if (n >= 8) {
+    store_raw8(p, round8(v, T{}));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = from_f32<T>(v[j]);
+  }
+}
+// Rounds 8 values to T and back (what a later read of the stored tensor sees).
+template <typename T>
+__device__ __forceinline__ void through8(float v[8]) {
+  widen8f(round8(v, T{}), v);
+}
+// The parameters of columns c .. c + 7: type T, or float where wf32; NULL: fill.
+template <typename T>
+__device__ __forceinline__ void load_param8(const void* w, bool wf32, int64_t c, int n, float fill,
+                                            float v[8]) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = fill;
+  } else if (wf32) {
+    load8(static_cast<const float*>(w) + c, n, v);
+  } else {
+    load8(static_cast<const T*>(w) + c, n, v);
+  }
+}
+__device__ __forceinline__ void zero_from8(int n, float v[8]) {
+  if (n < 8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j >= n) v[j] = 0.0f;
+  }
+}
+
+// ------------------------------------------------------------------ reductions
+// Wave-wide sum / unsigned max on the DPP network (no LDS): shifts inside rows
+// of 16 lanes, then the row broadcasts; the total lands in lane 63 and
+// comes back as a wave-uniform value.  Lanes without a source add zero.
+__device__ __forceinline__ float wave_sum(float x) {
+#define FP8DP_STEP(ctrl, rows)                                                              \
+  x += __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(x), ctrl, rows, 0xF, \
+                                                   false))
+  FP8DP_STEP(0x111, 0xF);   // row_shr:1
+  FP8DP_STEP(0x112, 0xF);   // row_shr:2
+  FP8DP_STEP(0x114, 0xF);   // row_shr:4
+  FP8DP_STEP(0x118, 0xF);   // row_shr:8
+  FP8DP_STEP(0x142, 0xA);   // row_bcast:15
+  FP8DP_STEP(0x143, 0xC);   // row_bcast:31
+#undef FP8DP_STEP
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 63));
+}
+__device__ __forceinline__ uint32_t wave_umax(uint32_t x) {
+#define FP8DP_STEP(ctrl, rows)                                                        \
+  do {                                                                                \
+    const uint32_t o = __builtin_amdgcn_update_dpp(0u, x, ctrl, rows, 0xF, false);    \
+    x = o > x ? o : x;                                                                \
+  } while (0)
+  FP8DP_STEP(0x111, 0xF);
+  FP8DP_STEP(0x112, 0xF);
+  FP8DP_STEP(0x114, 0xF);
+  FP8DP_STEP(0x118, 0xF);
+  FP8DP_STEP(0x142, 0xA);
+  FP8DP_STEP(0x143, 0xC);
+#undef FP8DP_STEP
+  return __builtin_amdgcn_readlane(x, 63);
+}
+
+// Totals over the THR threads of a row: a wave alone, or a workgroup through
+// LDS (scratch: one slot of THR / 64 values per call site).  Every thread
+// of the workgroup calls these together when THR > 64.
+template <int THR>
+__device__ __forceinline__ float row_sum(float x, float* scratch) {
+  x = wave_sum(x);
+  if constexpr (THR > 64) {
+    if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = 0.0f;
+#pragma unroll
+    for (int i = 0; i < THR / 64; ++i) x += scratch[i];
+  }
+  return x;
+}
+template <int THR>
+__device__ __forceinline__ uint32_t row_umax(uint32_t x, uint32_t* scratch) {
+  x = wave_umax(x);
+  if constexpr (THR > 64) {
+    if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = 0;
+#pragma unroll
+    for (int i = 0; i < THR / 64; ++i) x = scratch[i] > x ? scratch[i] : x;
+  }
+  return x;
+}
+
+// ------------------------------------------------------------------ dropout
+// Philox4x32 (Salmon et al., SC 2011), 10 rounds: per round two 32 x 32 -> 64
+// products and four XORs, the key advanced by the two Weyl constants.
+struct DropRule {
+  uint32_t threshold;     // kept: number >= threshold; 65536 drops all
+  float scale;            // 65536 / (65536 - threshold)
+};
+struct DropKey {
+  uint32_t k0, k1, c2, c3;
+};
+__device__ __forceinline__ DropKey drop_key(const uint64_t* rng) {
+  const uint64_t seed = rng[0], offset = rng[1];
+  return {(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)offset, (uint32_t)(offset >> 32)};
+}
+// x[j] = kept ? x[j] * scale : 0 for the 8 elements of vector `vec` of `row`.
+__device__ __forceinline__ void drop8(const DropKey& key, DropRule rule, uint32_t vec, uint32_t row,
+                                      float x[8]) {
+  uint32_t c0 = vec, c1 = row, c2 = key.c2, c3 = key.c3, k0 = key.k0, k1 = key.k1;
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t a = (uint64_t)0xD2511F53u * c0, b = (uint64_t)0xCD9E8D57u * c2;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c1 = (uint32_t)b;
+    c3 = (uint32_t)a;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  const uint32_t w[4] = {c0, c1, c2, c3};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = (w[j] & 0xFFFFu) >= rule.threshold ? x[2 * j] * rule.scale : 0.0f;
+    x[2 * j + 1] = (w[j] >> 16) >= rule.threshold ? x[2 * j + 1] * rule.scale : 0.0f;
+  }
+}
+// Host: the rule for p, and whether p is one.
+inline bool drop_rule(float p, DropRule* r) {
+  if (!(p >= 0.0f && p <= 1.0f)) return false;
+  r->threshold = (uint32_t)std::nearbyint((double)p * 65536.0);
+  r->scale = r->threshold < 65536u ? 65536.0f / (float)(65536u - r->threshold) : 0.0f;
+  return true;
+}
+
+// ------------------------------------------------------------------ INT8 codes
+// q = rint(127 x / m) for the row's largest magnitude m, ties to even, exactly.
+// up scales x and m by a power of two that keeps 127 x and 127 / m in
+// range.  t = x * fl(127 / m) is off by less than 2^-15, so q0 = rint(t) is right
+// unless t is next to a border between codes; there the remainder
+// r = 127 x - q0 m decides against m / 2.  Near a border r is exact: 127 x is split into
+// p and its rounding error e (zero for inputs of 16 bits), and p - q0 m loses its
+// leading bits.  The magic addend rounds to nearest even and leaves the code
+// in the low byte.
+struct RowScale {
+  float m, half, inv, up;   // m, m / 2, 127 / m after the scaling, the scaling
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
+  RowScale s;
+  float m = __uint_as_float(amax_bits);
+  s.up = m > 0x1p100f ? 0x1p-100f : (m < 0x1p-20f ? 0x1p100f : 1.0f);
+  s.m = m * s.up;
+  s.half = s.m * 0.5f;
+  s.inv = 127.0f / s.m;
+  return s;
+}
+// Packs the codes of 8 values (bytes in order).  The row's amax is finite and not zero.
+template <bool WIDE>
+__device__ __forceinline__ uint2 codes8(const float x[8], const RowScale& s) {
+  constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23
+  uint32_t b[8];
+  float worst = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float v = x[j] * s.up;
+    const float t = v * s.inv + kMagic;
+    b[j] = __float_as_uint(t);
+    const float r = __builtin_fmaf(-(t - kMagic), s.m, v * 127.0f);
+    worst = __builtin_fmaxf(worst, __builtin_fabsf(r));
+  }
+  // WIDE: r is off by up to half a unit of 127 x (2^-17 of a code step)
+  if (worst >= (WIDE ? s.half * 0.9999f : s.half)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float v = x[j] * s.up, p = v * 127.0f;
+      const float e = WIDE ? __builtin_fmaf(v, 127.0f, -p) : 0.0f;
+      const float q0 = __uint_as_float(b[j]) - kMagic;
+      const float r = __builtin_fmaf(-q0, s.m, p);
+      const float over = (__builtin_fabsf(r) - s.half) + (r < 0.0f ? -e : e);
+      if (over > 0.0f || (over == 0.0f && (b[j] & 1u))) b[j] += r < 0.0f ? -1 : 1;
+    }
+  }
+  uint2 q;
+  q.x = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0C0C0400u),
+                              __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u), 0x05040100u);
+  q.y = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[7], b[6], 0x0C0C0400u),
+                              __builtin_amdgcn_perm(b[5], b[4], 0x0C0C0400u), 0x05040100u);
+  return q;
+}
+__device__ __forceinline__ void store_codes8(int8_t* p, int n, uint2 q) {
+  if (n >= 8) {
+    *reinterpret_cast<u32x2_b_t*>(p) = u32x2_b_t{q.x, q.y};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = (int8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+  }
+}
+
+// ------------------------------------------------------------------ host checks
+inline int64_t dtype_size(fp8dp_dtype t) { return t == FP8DP_F32 ? 4 : 2; }
+inline bool known_dtype(fp8dp_dtype t) {
+  return t == FP8DP_BF16 || t == FP8DP_F16 || t == FP8DP_F32;
+}
+inline bool aligned_to(const void* p, int64_t n) {
+  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n - 1)) == 0;
+}
+inline int check_rows(const char* what, int64_t rows, int64_t cols) {
+  if (rows < 1 || cols < 1 || rows > 0x7FFFFFFF || cols > (1 << 30)) {
+    set_error("%s: rows must be 1 .. 2^31 - 1 and cols 1 .. 2^30 (got %lld, %lld)", what, (long long)rows,
+              (long long)cols);
+    return FP8DP_EINVAL;
+  }
+  return FP8DP_OK;
+}
+inline int check_types(const char* what, fp8dp_dtype dt, fp8dp_dtype wt) {
+  if (!known_dtype(dt) || !(wt == dt || wt == FP8DP_F32)) {
+    set_error("%s: unknown type, or parameters neither of the activations' type nor binary32", what);
+    return FP8DP_EINVAL;
+  }
+  return FP8DP_OK;
+}
+inline int bad_align(const char* what) {
+  set_error("%s: every pointer must be aligned to its elements", what);
+  return FP8DP_EINVAL;
+}
+
+}  // namespace fp8dp

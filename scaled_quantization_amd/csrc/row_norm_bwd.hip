@@ -1,0 +1,381 @@
+// row_norm_bwd.hip -- layer norm's backward pass, with the residual stream's
+// gradient added and the dropout mask applied again where asked.
+//
+//   g = dy w, h = (z - mean) rstd
+//   dz = rstd (g - mean(g) - h mean(g h)) + dz_add,  dx = keep dz / (1 - p)
+//   dw = sum over rows of dy h,  db = sum over rows of dy
+//
+// One pass: a persistent grid walks the rows, a wave or workgroup per row as in
+// the forward kernels, and each thread keeps the weight gradients of its own
+// columns in registers over all its rows.  The partial sums of a workgroup
+// go to the workspace once, and a second kernel adds them in a fixed order (no
+// atomics, so the same call gives the same bits).  dy and z are read once.
+#include <hip/hip_runtime.h>
+
+#include "row_core.hpp"
+
+namespace fp8dp {
+
+struct NormBwdArgs {
+  const void *dy, *z, *weight, *dz_add;
+  const float *mean, *rstd;
+  int64_t rows;
+  int cols;
+  bool wf32, sums;
+  DropRule rule;
+  const uint64_t* rng;
+  void *dz, *dx;
+  float* parts;        // [workgroups][2][cols]
+};
+
+// h and g of one vector.
+template <typename T>
+__device__ __forceinline__ void norm_hg(const float z[8], const float dy[8], const float w[8],
+                                        float mean, float rstd, float h[8], float g[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    h[j] = (z[j] - mean) * rstd;
+    g[j] = dy[j] * w[j];
+  }
+}
+
+template <typename T, bool DROP>
+__device__ __forceinline__ void norm_out(const NormBwdArgs& a, const DropKey& key, int64_t row,
+                                         int vec, int n, const float h[8], const float g[8],
+                                         float rstd, float mg, float mgh) {
+  const int64_t at = row * a.cols + (int64_t)vec * 8;
+  float d[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) d[j] = rstd * (g[j] - mg - h[j] * mgh);
+  if (a.dz_add != nullptr) {
+    float r[8];
+    load8(static_cast<const T*>(a.dz_add) + at, n, r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d[j] += r[j];
+  }
+  store8(static_cast<T*>(a.dz) + at, n, d);
+  if (a.dx != nullptr) {
+    if constexpr (DROP) drop8(key, a.rule, (uint32_t)vec, (uint32_t)row, d);
+    store8(static_cast<T*>(a.dx) + at, n, d);
+  }
+}
+
+// Sums of two values over the THR threads of a row, one barrier.
+template <int THR>
+__device__ __forceinline__ void row_sum2(float& x, float& y, float* scratch) {
+  x = wave_sum(x);
+  y = wave_sum(y);
+  if constexpr (THR > 64) {
+    if ((threadIdx.x & 63) == 0) {
+      scratch[2 * (threadIdx.x >> 6)] = x;
+      scratch[2 * (threadIdx.x >> 6) + 1] = y;
+    }
+    __syncthreads();
+    x = y = 0.0f;
+#pragma unroll
+    for (int i = 0; i < THR / 64; ++i) {
+      x += scratch[2 * i];
+      y += scratch[2 * i + 1];
+    }
+  }
+}
+
+constexpr int kBwdWaves = 8;   // waves of a workgroup whose waves own rows
+
+template <typename T, int NV, int THR, bool DROP>
+__global__ __launch_bounds__(THR == 64 ? 64 * kBwdWaves : THR) void k_norm_bwd(NormBwdArgs a) {
+  constexpr int RPB = THR == 64 ? kBwdWaves : 1;
+  __shared__ float lds[THR == 64 ? kBwdWaves / 2 * NV * 16 * 64 : 2 * 2 * (THR / 64)];
+  const int t = THR > 64 ? (int)threadIdx.x : (int)(threadIdx.x & 63);
+  const int sub = THR > 64 ? 0 : (int)(threadIdx.x >> 6);
+  const int cols = a.cols;
+  const float fcols = (float)cols;
+  DropKey key = {};
+  if constexpr (DROP) key = drop_key(a.rng);
+
+  float w[NV][8], dw[NV][8], db[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * THR + t) * 8;
+    load_param8<T>(a.weight, a.wf32, c, cols - c, 1.0f, w[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.0f;
+  }
+
+  int turn = 0;
+  for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < a.rows;
+       row += (int64_t)gridDim.x * RPB, turn ^= 1) {
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float h[NV][8], g[NV][8], sg = 0.0f, sgh = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * THR + t) * 8, n = cols - c;
+      const int64_t at = row * cols + c;
+      float z[8], dy[8];
+      load8(static_cast<const T*>(a.z) + at, n, z);
+      load8(static_cast<const T*>(a.dy) + at, n, dy);
+      norm_hg<T>(z, dy, w[i], mean, rstd, h[i], g[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sg += g[i][j];
+        sgh = __builtin_fmaf(g[i][j], h[i][j], sgh);
+        dw[i][j] = __builtin_fmaf(dy[j], h[i][j], dw[i][j]);
+        db[i][j] += dy[j];
+      }
+    }
+    row_sum2<THR>(sg, sgh, lds + (THR > 64 ? turn * 2 * (THR / 64) : 0));
+    const float mg = sg / fcols, mgh = sgh / fcols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int vec = i * THR + t, n = cols - vec * 8;
+      if (n > 0) norm_out<T, DROP>(a, key, row, vec, n, h[i], g[i], rstd, mg, mgh);
+    }
+  }
+  if (!a.sums) return;
+
+  if constexpr (THR == 64) {
+    // the waves' sums, halved in three steps through LDS (lane-major: no conflicts)
+#pragma unroll
+    for (int s = kBwdWaves / 2; s > 0; s >>= 1) {
+      __syncthreads();
+      if (sub >= s && sub < 2 * s) {
+        float* const o = lds + (sub - s) * NV * 16 * 64 + t;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            o[(i * 16 + j) * 64] = dw[i][j];
+            o[(i * 16 + 8 + j) * 64] = db[i][j];
+          }
+      }
+      __syncthreads();
+      if (sub < s) {
+        const float* const o = lds + sub * NV * 16 * 64 + t;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            dw[i][j] += o[(i * 16 + j) * 64];
+            db[i][j] += o[(i * 16 + 8 + j) * 64];
+          }
+      }
+    }
+    if (sub != 0) return;
+  }
+  float* const p = a.parts + (int64_t)blockIdx.x * 2 * cols;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * THR + t) * 8, n = cols - c;
+    if (n > 0) {
+      store8(p + c, n, dw[i]);
+      store8(p + cols + c, n, db[i]);
+    }
+  }
+}
+
+// Rows beyond the registers: dz by a workgroup per row, two reads of it; the
+// weight gradients by k_norm_bwd_cols, a thread per 8 columns down a range of rows.
+template <typename T, bool DROP>
+__global__ __launch_bounds__(1024) void k_norm_bwd_long(NormBwdArgs a) {
+  __shared__ float lds[2 * 2 * 16];
+  const int t = threadIdx.x, cols = a.cols;
+  const float fcols = (float)cols;
+  DropKey key = {};
+  if constexpr (DROP) key = drop_key(a.rng);
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float sg = 0.0f, sgh = 0.0f, mg = 0.0f, mgh = 0.0f;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      for (int64_t c = (int64_t)t * 8; c < cols; c += 8192) {
+        const int n = (int)(cols - c);
+        const int64_t at = row * cols + c;
+        float z[8], dy[8], w[8], h[8], g[8];
+        load8(static_cast<const T*>(a.z) + at, n, z);
+        load8(static_cast<const T*>(a.dy) + at, n, dy);
+        load_param8<T>(a.weight, a.wf32, c, n, 1.0f, w);
+        norm_hg<T>(z, dy, w, mean, rstd, h, g);
+        if (pass == 0) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            sg += g[j];
+            sgh = __builtin_fmaf(g[j], h[j], sgh);
+          }
+        } else {
+          norm_out<T, DROP>(a, key, row, (int)(c / 8), n, h, g, rstd, mg, mgh);
+        }
+      }
+      if (pass == 0) {
+        row_sum2<1024>(sg, sgh, lds + turn * 32);
+        mg = sg / fcols;
+        mgh = sgh / fcols;
+      }
+    }
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_norm_bwd_cols(NormBwdArgs a) {
+  const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  const int cols = a.cols, n = (int)(cols - c);
+  if (c >= cols) return;
+  float dw[8] = {}, db[8] = {};
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float z[8], dy[8];
+    load8(static_cast<const T*>(a.z) + row * cols + c, n, z);
+    load8(static_cast<const T*>(a.dy) + row * cols + c, n, dy);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      dw[j] = __builtin_fmaf(dy[j], (z[j] - mean) * rstd, dw[j]);
+      db[j] += dy[j];
+    }
+  }
+  float* const p = a.parts + (int64_t)blockIdx.y * 2 * cols;
+  store8(p + c, n, dw);
+  store8(p + cols + c, n, db);
+}
+
+// dweight and dbias from `parts` partial sums of 2 * cols values: 32 columns and 32
+// ranges of the sums per workgroup, the ranges joined in LDS in order.
+__global__ __launch_bounds__(1024) void k_norm_parts(const float* parts, int nparts, int cols,
+                                                     float* dweight, float* dbias) {
+  __shared__ float lds[32][33];
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+  const int64_t width = 2 * (int64_t)cols;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  float s = 0.0f;
+  if (c < width)
+    for (int i = group; i < nparts; i += 32) s += parts[i * width + c];
+  lds[group][lane] = s;
+  __syncthreads();
+  if (group == 0 && c < width) {
+    float total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) total += lds[i][lane];
+    if (c < cols) dweight[c] = total;
+    else dbias[c - cols] = total;
+  }
+}
+
+static int launch_parts(const NormBwdArgs& a, int nparts, float* dweight, float* dbias,
+                        hipStream_t stream) {
+  hipLaunchKernelGGL(k_norm_parts, dim3((unsigned)((2 * (int64_t)a.cols + 31) / 32)), dim3(1024), 0,
+                     stream, a.parts, nparts, a.cols, dweight, dbias);
+  return check_launch("layer_norm_backward");
+}
+
+template <typename T, int NV, int THR, bool DROP>
+static int launch_bwd(const NormBwdArgs& a, float* dweight, float* dbias, hipStream_t stream) {
+  constexpr int RPB = THR == 64 ? kBwdWaves : 1;
+  int64_t grid = (a.rows + RPB - 1) / RPB;
+  const int64_t cap = std::min<int64_t>(FP8DP_NORM_PARTS,
+                                        (int64_t)num_cus() * std::max(1, 1024 / (RPB * THR)));
+  if (grid > cap) grid = cap;
+  hipLaunchKernelGGL((k_norm_bwd<T, NV, THR, DROP>), dim3((unsigned)grid), dim3(RPB * THR), 0,
+                     stream, a);
+  const int rc = check_launch("layer_norm_backward");
+  if (rc || !a.sums) return rc;
+  return launch_parts(a, (int)grid, dweight, dbias, stream);
+}
+
+template <typename T, bool DROP>
+static int launch_bwd_long(const NormBwdArgs& a, float* dweight, float* dbias,
+                           hipStream_t stream) {
+  // the sums first: dz or dx may be written over dy
+  if (a.sums) {
+    const int64_t blocks = ((int64_t)a.cols + 2047) / 2048;
+    const int64_t want = std::max<int64_t>(1, (int64_t)num_cus() * 8 / blocks);
+    const int64_t parts = std::min<int64_t>({want, a.rows, FP8DP_NORM_PARTS});
+    hipLaunchKernelGGL((k_norm_bwd_cols<T>), dim3((unsigned)blocks, (unsigned)parts), dim3(256), 0,
+                       stream, a);
+    int rc = check_launch("layer_norm_backward");
+    if (rc || (rc = launch_parts(a, (int)parts, dweight, dbias, stream))) return rc;
+  }
+  hipLaunchKernelGGL((k_norm_bwd_long<T, DROP>),
+                     dim3((unsigned)std::min<int64_t>(a.rows, (int64_t)num_cus() * 8)), dim3(1024),
+                     0, stream, a);
+  return check_launch("layer_norm_backward");
+}
+
+template <typename T, bool DROP>
+static int launch_bwd_width(const NormBwdArgs& a, float* dweight, float* dbias,
+                            hipStream_t stream) {
+  const int64_t nvec = ((int64_t)a.cols + 7) / 8;
+  if (nvec <= 64) return launch_bwd<T, 1, 64, DROP>(a, dweight, dbias, stream);
+  if (nvec <= 128) return launch_bwd<T, 2, 64, DROP>(a, dweight, dbias, stream);
+  if (nvec <= 256) return launch_bwd<T, 1, 256, DROP>(a, dweight, dbias, stream);
+  if (nvec <= 512) return launch_bwd<T, 2, 256, DROP>(a, dweight, dbias, stream);
+  if (nvec <= 1024) return launch_bwd<T, 1, 1024, DROP>(a, dweight, dbias, stream);
+  if (nvec <= 2048) return launch_bwd<T, 2, 1024, DROP>(a, dweight, dbias, stream);
+  return launch_bwd_long<T, DROP>(a, dweight, dbias, stream);
+}
+
+template <bool DROP>
+static int launch_bwd_type(fp8dp_dtype dt, const NormBwdArgs& a, float* dweight, float* dbias,
+                           hipStream_t stream) {
+  if (dt == FP8DP_BF16) return launch_bwd_width<bf16_t, DROP>(a, dweight, dbias, stream);
+  if (dt == FP8DP_F16) return launch_bwd_width<f16_t, DROP>(a, dweight, dbias, stream);
+  return launch_bwd_width<float, DROP>(a, dweight, dbias, stream);
+}
+
+}  // namespace fp8dp
+
+using namespace fp8dp;
+
+extern "C" int layer_norm_backward(const void* dy, const void* z, const void* weight,
+                                   const float* mean, const float* rstd, const void* dz_add,
+                                   int64_t rows, int64_t cols, fp8dp_dtype dt, fp8dp_dtype wt,
+                                   float p, const uint64_t* rng, void* dz, void* dx,
+                                   float* dweight, float* dbias, float* workspace,
+                                   hipStream_t stream) {
+  const char* what = "layer_norm_backward";
+  int rc = check_rows(what, rows, cols);   // first: an empty tensor has no address
+  if (rc) return rc;
+  if (dy == nullptr || z == nullptr || mean == nullptr || rstd == nullptr || dz == nullptr) {
+    set_error("%s: dy, z, mean, rstd and dz must be non-NULL", what);
+    return FP8DP_EINVAL;
+  }
+  if ((dweight == nullptr) != (dbias == nullptr) || (dweight != nullptr && workspace == nullptr)) {
+    set_error("%s: dweight and dbias go together, and need a workspace", what);
+    return FP8DP_EINVAL;
+  }
+  NormBwdArgs a = {};
+  if ((rc = check_types(what, dt, wt))) return rc;
+  if (!drop_rule(p, &a.rule)) {
+    set_error("%s: p must be 0 .. 1", what);
+    return FP8DP_EINVAL;
+  }
+  if (dx != nullptr && p > 0.0f && rng == nullptr) {
+    set_error("%s: p > 0 needs rng (seed and offset on the device)", what);
+    return FP8DP_EINVAL;
+  }
+  const int64_t e = dtype_size(dt);
+  if (!aligned_to(dy, e) || !aligned_to(z, e) || !aligned_to(dz_add, e) || !aligned_to(dz, e) ||
+      !aligned_to(dx, e) || !aligned_to(weight, dtype_size(wt)) || !aligned_to(mean, 4) ||
+      !aligned_to(rstd, 4) || !aligned_to(dweight, 4) || !aligned_to(dbias, 4) ||
+      !aligned_to(workspace, 4) || !aligned_to(rng, 8))
+    return bad_align(what);
+  if (dz == dx || dz == z || dx == z) {
+    set_error("%s: dz, dx and z must be different buffers", what);
+    return FP8DP_EINVAL;
+  }
+  a.dy = dy;
+  a.z = z;
+  a.weight = weight;
+  a.dz_add = dz_add;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.rows = rows;
+  a.cols = (int)cols;
+  a.wf32 = wt == FP8DP_F32;
+  a.sums = dweight != nullptr;
+  a.rng = rng;
+  a.dz = dz;
+  a.dx = dx;
+  a.parts = workspace;
+  return dx != nullptr && a.rule.threshold > 0
+             ? launch_bwd_type<true>(dt, a, dweight, dbias, stream)
+             : launch_bwd_type<false>(dt, a, dweight, dbias, stream);
+}

@@ -23,6 +23,42 @@ struct I8Args {
   void* y;
 };
 
+// 16 bytes at any byte address.
+__device__ __forceinline__ v4i_t load16(const int8_t* p) {
+  const u32x4_b_t v = *reinterpret_cast<const u32x4_b_t*>(p);
+  return v4i_t{(int)v.x, (int)v.y, (int)v.z, (int)v.w};
+}
+
+// v with its first d bytes zero (d >= 16: all).
+__device__ __forceinline__ v4i_t zero_first(v4i_t v, int d) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int s = 8 * d - 32 * w;
+    v[w] &= s >= 32 ? 0 : s <= 0 ? -1 : (int)(0xFFFFFFFFu << s);
+  }
+  return v;
+}
+
+// A chunk of 16 bytes that K may cut.  The sum takes K in any order as long as
+// both operands agree, so a cut chunk is read as the row's last 16 bytes,
+// without reading past the row, and the bytes that earlier chunks hold already
+// are cleared in one operand (ONCE).  Rows below 16 bytes are read byte by byte.
+template <bool ONCE>
+__device__ __forceinline__ v4i_t load_chunk(const int8_t* row, int k, int K) {
+  if (K >= 16) {
+    const int at = k < K - 16 ? k : K - 16;
+    const v4i_t v = load16(row + at);
+    return ONCE ? zero_first(v, k - at) : v;
+  }
+  uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+  for (int j = 15; j >= 0; --j) {
+    hi = hi << 8 | lo >> 56;
+    lo = lo << 8 | (k + j < K ? (uint8_t)row[k + j] : 0);
+  }
+  return v4i_t{(int)lo, (int)(lo >> 32), (int)hi, (int)(hi >> 32)};
+}
+
 // Four outputs of row m, columns n .. n + 3, from their integer sums:
 // (sum sa) sb + bias in binary32, one rounding to T.  Columns at or past N are
 // not stored.
@@ -48,15 +84,40 @@ __device__ __forceinline__ void store_out4(const I8Args& g, int64_t m, int n, fl
       if (n + j < g.N) p[j] = from_f32<T>(v[j]);
   }
 }
+// Weight scales and bias of columns n .. n + 3, as loaded (clamped to the last
+// column) and widened, so that the loads can be issued long before their use.
+struct RawCols4 {
+  float sb[4];
+  uint32_t bias[4];
+};
 template <typename T>
-__device__ __forceinline__ void load_cols4(const I8Args& g, int n, float sb[4], float bias[4]) {
+__device__ __forceinline__ RawCols4 load_cols4(const I8Args& g, int n) {
+  RawCols4 r = {};
+  int c[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int c = n + j < g.N ? n + j : g.N - 1;
-    sb[j] = g.sb[c];
-    bias[j] = g.bias == nullptr ? 0.0f
-              : g.bias_f32      ? static_cast<const float*>(g.bias)[c]
-                                : to_f32(static_cast<const T*>(g.bias)[c]);
+    c[j] = n + j < g.N ? n + j : g.N - 1;
+    r.sb[j] = g.sb[c[j]];
+  }
+  if (g.bias != nullptr) {
+    if (sizeof(T) == 4 || g.bias_f32) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r.bias[j] = static_cast<const uint32_t*>(g.bias)[c[j]];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r.bias[j] = static_cast<const uint16_t*>(g.bias)[c[j]];
+    }
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void widen_bias4(const I8Args& g, const RawCols4& r, float bias[4]) {
+  if (sizeof(T) == 4 || g.bias_f32) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bias[j] = __uint_as_float(r.bias[j]);
+  } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bias[j] = to_f32(T{(uint16_t)r.bias[j]});
   }
 }
 

@@ -9,14 +9,15 @@
 #include <hip/hip_runtime.h>
 
 #include "int8_core.hpp"
+#include "int8_skinny.hpp"
+#include "int8_tile.hpp"
 
 namespace fp8dp {
 
 // ------------------------------------------------------------------ any shape
 // 64 x 64 outputs per workgroup of 4 waves (32 x 32 each, 2 x 2 of the
 // 16 x 16 x 64 instruction), K in stages of 128 bytes through registers into a
-// double-buffered LDS tile.  Rows may start at any byte; bytes past K are
-// read one by one in the last chunk and zeros beyond.
+// double-buffered LDS tile.  Rows may start at any byte and end at any.
 template <typename T>
 __global__ __launch_bounds__(256) void k_i8_any(I8Args g) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][64 * kBK];
@@ -37,31 +38,20 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args g) {
     pa[i] = g.a + (int64_t)(ra < g.M ? ra : g.M - 1) * g.lda;
     pb[i] = g.b + (int64_t)(rb < g.N ? rb : g.N - 1) * g.ldb;
   }
-  auto chunk = [&](const int8_t* row, int k) -> u32x4_t {
-    if (k + 16 <= g.K) {
-      const u32x4_b_t v = *reinterpret_cast<const u32x4_b_t*>(row + k);
-      return u32x4_t{v.x, v.y, v.z, v.w};
-    }
-    uint32_t w[4] = {};
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (k + j < g.K) w[j >> 2] |= (uint32_t)(uint8_t)row[k + j] << (8 * (j & 3));
-    return u32x4_t{w[0], w[1], w[2], w[3]};
-  };
-  u32x4_t ra[2], rb[2];
+  v4i_t ra[2], rb[2];
   auto load = [&](int s) {
     const int k = s * kBK + sch * 16;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      ra[i] = chunk(pa[i], k);
-      rb[i] = chunk(pb[i], k);
+      ra[i] = load_chunk<true>(pa[i], k, g.K);
+      rb[i] = load_chunk<false>(pb[i], k, g.K);
     }
   };
   auto put = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      *reinterpret_cast<u32x4_t*>(&lds[buf][0][swz(srow + 32 * i, sch)]) = ra[i];
-      *reinterpret_cast<u32x4_t*>(&lds[buf][1][swz(srow + 32 * i, sch)]) = rb[i];
+      *reinterpret_cast<v4i_t*>(&lds[buf][0][swz(srow + 32 * i, sch)]) = ra[i];
+      *reinterpret_cast<v4i_t*>(&lds[buf][1][swz(srow + 32 * i, sch)]) = rb[i];
     }
   };
 
@@ -94,12 +84,13 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args g) {
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int n = n0 + wn + 16 * j + 4 * fch;
-    float sb[4], bias[4];
-    load_cols4<T>(g, n, sb, bias);
+    const RawCols4 cols = load_cols4<T>(g, n);
+    float bias[4];
+    widen_bias4<T>(g, cols, bias);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int m = m0 + wm + 16 * i + frow;
-      if (m < g.M) store_out4<T>(g, m, n, g.sa[m], sb, bias, acc[i][j]);
+      if (m < g.M) store_out4<T>(g, m, n, g.sa[m], cols.sb, bias, acc[i][j]);
     }
   }
 }
@@ -118,6 +109,8 @@ static int launch_i8(const char* what, const I8Args& g, void* workspace, int64_t
 
 static int dispatch_i8(const char* what, fp8dp_dtype yt, const I8Args& g, void* workspace,
                        int64_t workspace_bytes, hipStream_t stream) {
+  if (g.M <= 64 && g.K >= 128) return skinny_i8(what, yt, g, nullptr, stream);
+  if (tile_takes(g)) return tile_i8(what, yt, g, stream);
   if (yt == FP8DP_BF16) return launch_i8<bf16_t>(what, g, workspace, workspace_bytes, stream);
   if (yt == FP8DP_F16) return launch_i8<f16_t>(what, g, workspace, workspace_bytes, stream);
   return launch_i8<float>(what, g, workspace, workspace_bytes, stream);
@@ -190,6 +183,11 @@ extern "C" int int8_linear(const void* x, const int8_t* w8, const float* w_scale
   if (!aligned_to(x, dtype_size(dt)) || !aligned_to(w_scale, 4) || !aligned_to(y, dtype_size(dt)) ||
       !aligned_to(bias, dtype_size(bt)))
     return bad_align(what);
+  if (skinny_casts(M, K)) {
+    const I8Args g = {nullptr, w8, (int)M, (int)N, (int)K, K, K, nullptr, w_scale, bias,
+                      bt == FP8DP_F32, y};
+    return skinny_i8(what, dt, g, x, stream);
+  }
   const int64_t ld = padded_k(K);
   int8_t* const q = static_cast<int8_t*>(workspace);
   float* const scale = reinterpret_cast<float*>(q + M * ld);

@@ -1,0 +1,212 @@
+// int8_tile.hip -- the INT8 product in LDS tiles, for operands whose rows start at
+// multiples of 16 bytes (K itself a multiple of 16).
+//
+// A workgroup of WM x WN waves owns BM x BN outputs; a wave TM x TN tiles of
+// the 32 x 32 x 32 matrix instruction.  K advances 128 bytes per stage through a
+// ring of S slots in LDS, which global_load_lds fills without passing registers
+// (16-byte chunks swizzled as gemm_core.hpp describes, so that fragment reads
+// meet no bank twice).  Software pipeline by half stages, fragments
+// double-buffered: the first half of a stage reads its second 64 bytes of K while
+// the first are multiplied; then one barrier shows that every wave's copies of
+// the next stage have landed and that this stage's slot has been read; the
+// second half refills the slot, reads the next stage's first 64 bytes and
+// multiplies the second.
+// Rows past M or N are read as the last row and not stored; chunks past K come as
+// zeros for the tokens and as any chunk of the row for the weight.
+#include <hip/hip_runtime.h>
+
+#include "int8_core.hpp"
+#include "int8_tile.hpp"
+
+namespace fp8dp {
+
+__device__ const u32x4_t kZeroChunk = {0, 0, 0, 0};
+
+// Lane i's 16 bytes at base + off[i] land at l + 16 i; as copy16_to_lds, with
+// the wave's base in scalar registers.
+__device__ __forceinline__ void copy16_to_lds_at(const int8_t* base, uint32_t off, uint8_t* l) {
+  const uint32_t la = (uint32_t)(uintptr_t)(lds_void_t*)l;
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(off), "s"(base), "{m0}"(la)
+               : "memory");
+}
+
+template <typename T, int WM, int WN, int TM, int TN, int S>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_i8_tile(I8Args g) {
+  constexpr int W = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
+  constexpr int ASZ = BM * kBK, SLOT = (BM + BN) * kBK;
+  static_assert(W % 2 == 0, "the swizzle of a copy");
+  constexpr int LA = BM / 8 / W, LB = BN / 8 / W, NCOPY = LA + LB;   // copies of a wave per stage
+  __shared__ __attribute__((aligned(16))) uint8_t lds[S * SLOT];
+
+  const int tiles_n = (g.N + BN - 1) / BN;
+  const int ntiles = ((g.M + BM - 1) / BM) * tiles_n;
+  const int tile = tile_of_block(blockIdx.x, ntiles);
+  const int m0 = (tile / tiles_n) * BM, n0 = (tile % tiles_n) * BN;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = (wave / WN) * TM * 32, wc = (wave % WN) * TN * 32;
+  const int KT = (g.K + kBK - 1) / kBK;
+
+  // copy i of this wave: rows 8 (wave + W i) .. + 7 of the tile, lane l the logical chunk that
+  // swz() places at chunk l % 8 of row l / 8
+  const int lrow = lane >> 3;
+  const int8_t* const baseA = g.a + (int64_t)m0 * g.lda;
+  const int8_t* const baseB = g.b + (int64_t)n0 * g.ldb;
+  uint32_t offA[LA], offB[LB];
+  // (r / 2) % 8 of row r = 8 (wave + W i) + l / 8 does not depend on i
+  const int chunk = (lane & 7) ^ ((4 * wave + (lrow >> 1)) & 7);
+#pragma unroll
+  for (int i = 0; i < LA; ++i) {
+    const int r = 8 * (wave + W * i) + lrow;
+    offA[i] = (uint32_t)((r < g.M - m0 ? r : g.M - 1 - m0) * (uint32_t)g.lda + chunk * 16);
+  }
+#pragma unroll
+  for (int i = 0; i < LB; ++i) {
+    const int r = 8 * (wave + W * i) + lrow;
+    offB[i] = (uint32_t)((r < g.N - n0 ? r : g.N - 1 - n0) * (uint32_t)g.ldb + chunk * 16);
+  }
+  auto issue = [&](int kt) {
+    uint8_t* const base = lds + (kt % S) * SLOT + wave * 1024;
+    const int k0 = kt * kBK;
+    if (k0 + kBK <= g.K) {
+#pragma unroll
+      for (int i = 0; i < LA; ++i)
+        copy16_to_lds_at(baseA + k0, offA[i], base + i * W * 1024);
+#pragma unroll
+      for (int i = 0; i < LB; ++i)
+        copy16_to_lds_at(baseB + k0, offB[i], base + ASZ + i * W * 1024);
+    } else {
+      const int left = (g.K - k0) / 16;   // chunks of this stage inside K, 1 .. 7
+#pragma unroll
+      for (int i = 0; i < LA; ++i)
+        copy16_to_lds(chunk < left
+                          ? reinterpret_cast<const uint8_t*>(baseA + k0 + offA[i])
+                          : reinterpret_cast<const uint8_t*>(&kZeroChunk),
+                      base + i * W * 1024);
+#pragma unroll
+      for (int i = 0; i < LB; ++i)
+        copy16_to_lds(reinterpret_cast<const uint8_t*>(
+                          baseB + k0 + offB[i] - (chunk < left ? 0 : chunk * 16)),
+                      base + ASZ + i * W * 1024);
+    }
+  };
+
+  const int frow = lane & 31, fhalf = lane >> 5;
+  // 64 bytes of K (half h of a stage) as two 32-byte steps
+  auto load_frags = [&](int kt, int h, v4i_t (&fa)[2][TM], v4i_t (&fb)[2][TN]) {
+    const uint8_t* const sA = lds + (kt % S) * SLOT;
+    const uint8_t* const sB = sA + ASZ;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int c = h * 4 + q * 2 + fhalf;
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+        fa[q][i] = *reinterpret_cast<const v4i_t*>(sA + swz(wr + 32 * i + frow, c));
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        fb[q][j] = *reinterpret_cast<const v4i_t*>(sB + swz(wc + 32 * j + frow, c));
+    }
+  };
+  v16i_t acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+  auto multiply = [&](const v4i_t (&fa)[2][TM], const v4i_t (&fb)[2][TN]) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[q][j], fa[q][i], acc[i][j], 0, 0, 0);
+  };
+
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+    if (s < KT) issue(s);
+  if (KT >= S) wait_vmcnt<(S - 1) * NCOPY>();
+  else wait_vmcnt<0>();
+  stage_barrier();
+
+  v4i_t fa0[2][TM], fb0[2][TN], fa1[2][TM], fb1[2][TN];
+  load_frags(0, 0, fa0, fb0);
+  for (int kt = 0; kt < KT; ++kt) {
+    load_frags(kt, 1, fa1, fb1);
+    multiply(fa0, fb0);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's reads of stage kt are done
+    if (kt + S - 1 < KT) wait_vmcnt<(S - 2) * NCOPY>();   // its copies of stage kt + 1 have landed
+    else wait_vmcnt<0>();
+    stage_barrier();
+    if (kt + S < KT) issue(kt + S);
+    if (kt + 1 < KT) load_frags(kt + 1, 0, fa0, fb0);
+    multiply(fa1, fb1);
+  }
+
+  // a 32 x 32 tile: lane holds token lane % 32, register r channel 8 (r / 4) + 4 (lane / 32) + r % 4
+  float sa[TM];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int m = m0 + wr + 32 * i + frow;
+    sa[i] = g.sa[m < g.M ? m : g.M - 1];
+  }
+#pragma unroll
+  for (int j = 0; j < TN; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int n = n0 + wc + 32 * j + 8 * q + 4 * fhalf;
+      if (n >= g.N) continue;
+      const RawCols4 cols = load_cols4<T>(g, n);
+      float bias[4];
+      widen_bias4<T>(g, cols, bias);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const int m = m0 + wr + 32 * i + frow;
+        const v4i_t c = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                         acc[i][j][4 * q + 3]};
+        if (m < g.M) store_out4<T>(g, m, n, sa[i], cols.sb, bias, c);
+      }
+    }
+}
+
+template <typename T, int WM, int WN, int TM, int TN, int S>
+static int launch_tile(const char* what, const I8Args& g, hipStream_t stream) {
+  constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
+  const int64_t tiles = (((int64_t)g.M + BM - 1) / BM) * (((int64_t)g.N + BN - 1) / BN);
+  if (tiles > 0x7FFFFFFF) {
+    set_error("%s: shape too large", what);
+    return FP8DP_EINVAL;
+  }
+  hipLaunchKernelGGL((k_i8_tile<T, WM, WN, TM, TN, S>), dim3((unsigned)tiles), dim3(64 * WM * WN),
+                     0, stream, g);
+  return check_launch(what);
+}
+
+template <typename T>
+static int tile_type(const char* what, const I8Args& g, hipStream_t stream) {
+  // the largest tile that still gives every compute unit one
+  auto tiles = [&](int bm, int bn) {
+    return (((int64_t)g.M + bm - 1) / bm) * (((int64_t)g.N + bn - 1) / bn);
+  };
+  const int64_t cus = num_cus();
+  if (tiles(256, 256) >= cus) return launch_tile<T, 4, 2, 2, 4, 2>(what, g, stream);
+  if (tiles(128, 128) >= cus) return launch_tile<T, 2, 2, 2, 2, 2>(what, g, stream);
+  return launch_tile<T, 2, 2, 1, 1, 4>(what, g, stream);
+}
+
+bool tile_takes(const I8Args& g) {
+  return g.K % 16 == 0 && g.lda % 16 == 0 && g.ldb % 16 == 0 && aligned16(g.a) && aligned16(g.b);
+}
+
+int tile_i8(const char* what, fp8dp_dtype yt, const I8Args& g, hipStream_t stream) {
+  if (yt == FP8DP_BF16) return tile_type<bf16_t>(what, g, stream);
+  if (yt == FP8DP_F16) return tile_type<f16_t>(what, g, stream);
+  return tile_type<float>(what, g, stream);
+}
+
+}  // namespace fp8dp

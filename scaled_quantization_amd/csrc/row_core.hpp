@@ -112,16 +112,111 @@ __device__ __forceinline__ void store_raw8<float>(float* p, const Raw8<float>& r
   *reinterpret_cast<f32x4_e_t*>(p + 4) = r.hi;
 }
 
-// The n elements at p (n >= 8: 8 of them; n <= 0: none), the rest zeros.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, float v[8]) {
-  if (n >= 8) {
-    widen8f(load_raw8(p), v);
-  } else {
+// The n elements at p (n >= 8: 8 of them; n <= 0: none), the rest zeros, still as loaded:
+// nothing waits for them before they are widened, so several vectors travel
+// together.  A cut vector takes 8 loads of single elements, clamped instead of branched over.
+__device__ __forceinline__ void load_cut(const bf16_t* p, int n, Raw8<bf16_t>& r) {
+  const uint16_t* const q = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? to_f32(p[j]) : 0.0f;
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t lo = q[2 * j < n ? 2 * j : 0], hi = q[2 * j + 1 < n ? 2 * j + 1 : 0];
+    r.w[j] = (2 * j < n ? lo : 0u) | (2 * j + 1 < n ? hi << 16 : 0u);
   }
 }
+__device__ __forceinline__ void load_cut(const f16_t* p, int n, Raw8<f16_t>& r) {
+  Raw8<bf16_t> b;
+  load_cut(reinterpret_cast<const bf16_t*>(p), n, b);
+  r.w = b.w;
+}
+__device__ __forceinline__ void load_cut(const float* p, int n, Raw8<float>& r) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float lo = p[j < n ? j : 0], hi = p[j + 4 < n ? j + 4 : 0];
+    r.lo[j] = j < n ? lo : 0.0f;
+    r.hi[j] = j + 4 < n ? hi : 0.0f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw(const T* p, int n) {
+  Raw8<T> r = {};
+  if (n >= 8) r = load_raw8(p);
+  else if (n > 0) load_cut(p, n, r);
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int n, float v[8]) {
+  widen8f(load_raw(p, n), v);
+}
+
+// The same for rows of at least 8 elements, without a branch: the vector at
+// column c is read at min(c, cols - 8), and settle() moves a cut one's n elements
+// to the front and clears the rest once they have arrived.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_row(const T* row, int c, int cols) {
+  return load_raw8(row + (c < cols - 8 ? c : cols - 8));
+}
+__device__ __forceinline__ u32x4_e_t shift_down(u32x4_e_t w, int s) {   // by s bits, s > 0
+  uint64_t lo = (uint64_t)w[1] << 32 | w[0], hi = (uint64_t)w[3] << 32 | w[2];
+  lo = s < 64 ? lo >> s | hi << (64 - s) : s < 128 ? hi >> (s - 64) : 0;
+  hi = s < 64 ? hi >> s : 0;
+  return u32x4_e_t{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+__device__ __forceinline__ void settle(Raw8<bf16_t>& r, int n) {
+  if (n < 8) r.w = shift_down(r.w, n > 0 ? 16 * (8 - n) : 128);
+}
+__device__ __forceinline__ void settle(Raw8<f16_t>& r, int n) {
+  if (n < 8) r.w = shift_down(r.w, n > 0 ? 16 * (8 - n) : 128);
+}
+__device__ __forceinline__ void settle(Raw8<float>& r, int n) {
+  if (n < 8) {
+    float v[8] = {r.lo[0], r.lo[1], r.lo[2], r.lo[3], r.hi[0], r.hi[1], r.hi[2], r.hi[3]};
+    const int s = n > 0 ? 8 - n : 8;
+#pragma unroll
+    for (int b = 1; b <= 8; b <<= 1)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (s & b) v[j] = j + b < 8 ? v[j + b] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      r.lo[j] = v[j];
+      r.hi[j] = v[j + 4];
+    }
+  }
+}
+// Parameters of the vector at column c as loaded: type T, or float where wf32.
+struct RawParam {
+  f32x4_e_t lo, hi;
+};
+template <typename T>
+__device__ __forceinline__ RawParam load_param(const void* w, bool wf32, int c, int cols) {
+  RawParam r = {};
+  if (w == nullptr) return r;
+  if (sizeof(T) == 4 || wf32) {
+    const Raw8<float> f = load_row(static_cast<const float*>(w), c, cols);
+    r.lo = f.lo;
+    r.hi = f.hi;
+  } else if constexpr (sizeof(T) == 2) {
+    r.lo = __builtin_bit_cast(f32x4_e_t, load_row(static_cast<const T*>(w), c, cols).w);
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void widen_param(const RawParam& r, const void* w, bool wf32, int n,
+                                            float fill, float v[8]) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = fill;
+  } else if (sizeof(T) == 4 || wf32) {
+    Raw8<float> f = {r.lo, r.hi};
+    settle(f, n);
+    widen8f(f, v);
+  } else if constexpr (sizeof(T) == 2) {
+    Raw8<T> h = {__builtin_bit_cast(u32x4_e_t, r.lo)};
+    settle(h, n);
+    widen8f(h, v);
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ void store8(T* p, int n, const float v[8]) {
   if (n >= 8) {

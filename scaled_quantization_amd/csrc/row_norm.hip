@@ -32,20 +32,23 @@ struct RowArgs {
 };
 
 // T: element type.  NV vectors of 8 per thread in registers (0: a loop over longer
-// rows).  THR threads per row.  DROP: apply the mask.  NORM / QUANT: the norm,
-// the cast.  Without both, z (or out) is all there is to write.
+// rows, and rows of less than 8).  THR threads per row.  DROP: apply the mask.  NORM / QUANT:
+// the norm, the cast.  Without both, z (or out) is all there is to write.
 template <typename T, int NV, int THR, bool DROP, bool NORM, bool QUANT>
 __global__ __launch_bounds__(THR < 256 ? 256 : THR) void k_row(RowArgs a) {
   constexpr int RPB = THR < 256 ? 256 / THR : 1;   // rows per workgroup
   constexpr bool REG = NV > 0;
+  constexpr int HELD = REG ? NV : 1;
   constexpr int WAVES = THR / 64;
   __shared__ float scratch[THR > 64 ? 2 * 3 * WAVES : 1];
   const int t = THR > 64 ? (int)threadIdx.x : (int)(threadIdx.x & 63);
-  const int sub = THR > 64 ? 0 : (int)(threadIdx.x >> 6);
+  const int sub = THR > 64 ? 0 : (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cols = a.cols;
   const int nvec = (int)(((QUANT ? a.ldq : (int64_t)cols) + 7) / 8);
   const int steps = REG ? NV : (nvec + THR - 1) / THR;
   const float fcols = (float)cols;
+  const T* const x = static_cast<const T*>(a.x);
+  const T* const residual = static_cast<const T*>(a.residual);
   DropKey key = {};
   if constexpr (DROP) key = drop_key(a.rng);
 
@@ -54,16 +57,16 @@ __global__ __launch_bounds__(THR < 256 ? 256 : THR) void k_row(RowArgs a) {
        row += (int64_t)gridDim.x * RPB, turn ^= 1) {
     float* const sc = scratch + (THR > 64 ? turn * 3 * WAVES : 0);
     const int64_t base = row * cols;
-    float v[REG ? NV : 1][8];
+    auto column = [&](int i) { return (i * THR + t) * 8; };
+    float v[HELD][8];
+    float sum = 0.0f;
+    uint32_t top = 0;
 
-    // the row's values, from the inputs
-    auto first = [&](int i, float* w) {
-      const int vec = i * THR + t, c = vec * 8, n = cols - c;
-      load8(static_cast<const T*>(a.x) + base + c, n, w);
-      if constexpr (DROP) drop8(key, a.rule, (uint32_t)vec, (uint32_t)row, w);
-      if (a.residual != nullptr) {
-        float r[8];
-        load8(static_cast<const T*>(a.residual) + base + c, n, r);
+    // one vector of the row: mask, residual sum, z, and its part of the first statistic
+    auto begin = [&](int i, float* w, const float* r) {
+      const int c = column(i), n = cols - c;
+      if constexpr (DROP) drop8(key, a.rule, (uint32_t)(i * THR + t), (uint32_t)row, w);
+      if (residual != nullptr) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] += r[j];
       }
@@ -71,28 +74,6 @@ __global__ __launch_bounds__(THR < 256 ? 256 : THR) void k_row(RowArgs a) {
         through8<T>(w);
         store8(static_cast<T*>(a.z) + base + c, n, w);
       }
-    };
-    // the same values once more (long rows)
-    auto again = [&](int i, float* w) {
-      const int c = (i * THR + t) * 8;
-      load8(static_cast<const T*>(a.z != nullptr ? a.z : a.x) + base + c, cols - c, w);
-    };
-    auto each = [&](auto&& f) {
-      if constexpr (REG) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) f(i, v[i]);
-      } else {
-        for (int i = 0; i < steps; ++i) {
-          again(i, v[0]);
-          f(i, v[0]);
-        }
-      }
-    };
-
-    float sum = 0.0f;
-    uint32_t top = 0;
-    auto add_first = [&](int i, float* w) {
-      first(i, w);
       if constexpr (NORM) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum += w[j];
@@ -104,22 +85,76 @@ __global__ __launch_bounds__(THR < 256 ? 256 : THR) void k_row(RowArgs a) {
         }
       }
     };
+    // parameters of a vector: held as loaded (issued ahead of the row), or loaded at their use
+    RawParam pw[HELD], pb[HELD];
+    auto params = [&](int i, int n, float* g, float* b) {
+      if constexpr (REG) {
+        widen_param<T>(pw[i], a.weight, a.wf32, n, 1.0f, g);
+        widen_param<T>(pb[i], a.bias, a.wf32, n, 0.0f, b);
+      } else {
+        load_param8<T>(a.weight, a.wf32, column(i), n, 1.0f, g);
+        load_param8<T>(a.bias, a.wf32, column(i), n, 0.0f, b);
+      }
+    };
     if constexpr (REG) {
+      // every load of the row first, without a branch, then the arithmetic
+      Raw8<T> rx[NV], rr[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) add_first(i, v[i]);
+      for (int i = 0; i < NV; ++i) rx[i] = load_row(x + base, column(i), cols);
+      if (residual != nullptr) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) rr[i] = load_row(residual + base, column(i), cols);
+      }
+      if constexpr (NORM) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          pw[i] = load_param<T>(a.weight, a.wf32, column(i), cols);
+          pb[i] = load_param<T>(a.bias, a.wf32, column(i), cols);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int n = cols - column(i);
+        float r[8] = {};
+        settle(rx[i], n);
+        widen8f(rx[i], v[i]);
+        if (residual != nullptr) {
+          settle(rr[i], n);
+          widen8f(rr[i], r);
+        }
+        begin(i, v[i], r);
+      }
     } else {
-      for (int i = 0; i < steps; ++i) add_first(i, v[0]);
+      for (int i = 0; i < steps; ++i) {
+        const int c = column(i), n = cols - c;
+        float r[8] = {};
+        load8(x + base + c, n, v[0]);
+        if (residual != nullptr) load8(residual + base + c, n, r);
+        begin(i, v[0], r);
+      }
     }
+    // f(i, values): from the registers, or read again
+    auto each = [&](auto&& f) {
+      if constexpr (REG) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) f(i, v[i]);
+      } else {
+        const T* const from = a.z != nullptr ? static_cast<const T*>(a.z) : x;
+        for (int i = 0; i < steps; ++i) {
+          load8(from + base + column(i), cols - column(i), v[0]);
+          f(i, v[0]);
+        }
+      }
+    };
 
     float mean = 0.0f, rstd = 0.0f;
     if constexpr (NORM) {
       mean = row_sum<THR>(sum, sc) / fcols;
       float sq = 0.0f;
       each([&](int i, float* w) {
-        const int n = cols - (i * THR + t) * 8;
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] -= mean;
-        zero_from8(n, w);
+        zero_from8(cols - column(i), w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(w[j], w[j], sq);
       });
@@ -131,10 +166,9 @@ __global__ __launch_bounds__(THR < 256 ? 256 : THR) void k_row(RowArgs a) {
       }
       // in registers the row is now x - mean; read again it is x
       each([&](int i, float* w) {
-        const int c = (i * THR + t) * 8, n = cols - c;
+        const int c = column(i), n = cols - c;
         float g[8], b[8];
-        load_param8<T>(a.weight, a.wf32, c, n, 1.0f, g);
-        load_param8<T>(a.bias, a.wf32, c, n, 0.0f, b);
+        params(i, n, g, b);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           w[j] = __builtin_fmaf((REG ? w[j] : w[j] - mean) * rstd, g[j], b[j]);
@@ -160,11 +194,10 @@ __global__ __launch_bounds__(THR < 256 ? 256 : THR) void k_row(RowArgs a) {
                              : (top == 0 ? 0.0f : __builtin_nanf(""));
       int8_t* const q = a.q + row * a.ldq;
       each([&](int i, float* w) {
-        const int c = (i * THR + t) * 8, n = cols - c;
+        const int c = column(i), n = cols - c;
         if constexpr (NORM && !REG) {
           float g[8], b[8];
-          load_param8<T>(a.weight, a.wf32, c, n, 1.0f, g);
-          load_param8<T>(a.bias, a.wf32, c, n, 0.0f, b);
+          params(i, n, g, b);
 #pragma unroll
           for (int j = 0; j < 8; ++j) w[j] = __builtin_fmaf((w[j] - mean) * rstd, g[j], b[j]);
           zero_from8(n, w);
@@ -192,6 +225,7 @@ static int launch_row(const RowArgs& a, const char* what, hipStream_t stream) {
 template <typename T, bool DROP, bool NORM, bool QUANT>
 static int launch_width(const RowArgs& a, const char* what, hipStream_t stream) {
   const int64_t nvec = ((QUANT ? a.ldq : (int64_t)a.cols) + 7) / 8;
+  if (a.cols < 8) return launch_row<T, 0, 64, DROP, NORM, QUANT>(a, what, stream);
   if (nvec <= 64) return launch_row<T, 1, 64, DROP, NORM, QUANT>(a, what, stream);
   if (nvec <= 128) return launch_row<T, 2, 64, DROP, NORM, QUANT>(a, what, stream);
   if (nvec <= 256) return launch_row<T, 4, 64, DROP, NORM, QUANT>(a, what, stream);

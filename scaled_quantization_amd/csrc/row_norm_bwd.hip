@@ -29,7 +29,6 @@ struct NormBwdArgs {
 };
 
 // h and g of one vector.
-template <typename T>
 __device__ __forceinline__ void norm_hg(const float z[8], const float dy[8], const float w[8],
                                         float mean, float rstd, float h[8], float g[8]) {
 #pragma unroll
@@ -42,16 +41,14 @@ __device__ __forceinline__ void norm_hg(const float z[8], const float dy[8], con
 template <typename T, bool DROP>
 __device__ __forceinline__ void norm_out(const NormBwdArgs& a, const DropKey& key, int64_t row,
                                          int vec, int n, const float h[8], const float g[8],
-                                         float rstd, float mg, float mgh) {
+                                         const float add[8], float rstd, float mg, float mgh) {
   const int64_t at = row * a.cols + (int64_t)vec * 8;
   float d[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) d[j] = rstd * (g[j] - mg - h[j] * mgh);
   if (a.dz_add != nullptr) {
-    float r[8];
-    load8(static_cast<const T*>(a.dz_add) + at, n, r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) d[j] += r[j];
+    for (int j = 0; j < 8; ++j) d[j] += add[j];
   }
   store8(static_cast<T*>(a.dz) + at, n, d);
   if (a.dx != nullptr) {
@@ -87,48 +84,77 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBwdWaves : THR) void k_norm_bwd(N
   constexpr int RPB = THR == 64 ? kBwdWaves : 1;
   __shared__ float lds[THR == 64 ? kBwdWaves / 2 * NV * 16 * 64 : 2 * 2 * (THR / 64)];
   const int t = THR > 64 ? (int)threadIdx.x : (int)(threadIdx.x & 63);
-  const int sub = THR > 64 ? 0 : (int)(threadIdx.x >> 6);
+  const int sub = THR > 64 ? 0 : (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cols = a.cols;
   const float fcols = (float)cols;
+  const T *const z = static_cast<const T*>(a.z), *const dy = static_cast<const T*>(a.dy),
+          *const add = static_cast<const T*>(a.dz_add);
   DropKey key = {};
   if constexpr (DROP) key = drop_key(a.rng);
+  auto column = [&](int i) { return (i * THR + t) * 8; };
+
+  // the row in hand and the next one, still as loaded: a row's loads have a whole
+  // row of arithmetic to arrive
+  struct Row {
+    Raw8<T> z[NV], dy[NV], add[NV];
+    float mean, rstd;
+  };
+  auto load = [&](int64_t row, Row& r) {
+    const int64_t base = (row < a.rows ? row : a.rows - 1) * cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      r.z[i] = load_row(z + base, column(i), cols);
+      r.dy[i] = load_row(dy + base, column(i), cols);
+      if (add != nullptr) r.add[i] = load_row(add + base, column(i), cols);
+    }
+    r.mean = a.mean[row < a.rows ? row : a.rows - 1];
+    r.rstd = a.rstd[row < a.rows ? row : a.rows - 1];
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB, first = (int64_t)blockIdx.x * RPB + sub;
+  Row next;
+  load(first, next);
 
   float w[NV][8], dw[NV][8], db[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * THR + t) * 8;
-    load_param8<T>(a.weight, a.wf32, c, cols - c, 1.0f, w[i]);
+    load_param8<T>(a.weight, a.wf32, column(i), cols - column(i), 1.0f, w[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.0f;
   }
 
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < a.rows;
-       row += (int64_t)gridDim.x * RPB, turn ^= 1) {
-    const float mean = a.mean[row], rstd = a.rstd[row];
+  for (int64_t row = first; row < a.rows; row += step, turn ^= 1) {
+    Row r = next;
+    load(row + step, next);
     float h[NV][8], g[NV][8], sg = 0.0f, sgh = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * THR + t) * 8, n = cols - c;
-      const int64_t at = row * cols + c;
-      float z[8], dy[8];
-      load8(static_cast<const T*>(a.z) + at, n, z);
-      load8(static_cast<const T*>(a.dy) + at, n, dy);
-      norm_hg<T>(z, dy, w[i], mean, rstd, h[i], g[i]);
+      const int n = cols - column(i);
+      float vz[8], vd[8];
+      settle(r.z[i], n);
+      settle(r.dy[i], n);
+      widen8f(r.z[i], vz);
+      widen8f(r.dy[i], vd);
+      norm_hg(vz, vd, w[i], r.mean, r.rstd, h[i], g[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         sg += g[i][j];
         sgh = __builtin_fmaf(g[i][j], h[i][j], sgh);
-        dw[i][j] = __builtin_fmaf(dy[j], h[i][j], dw[i][j]);
-        db[i][j] += dy[j];
+        dw[i][j] = __builtin_fmaf(vd[j], h[i][j], dw[i][j]);
+        db[i][j] += vd[j];
       }
     }
     row_sum2<THR>(sg, sgh, lds + (THR > 64 ? turn * 2 * (THR / 64) : 0));
     const float mg = sg / fcols, mgh = sgh / fcols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int vec = i * THR + t, n = cols - vec * 8;
-      if (n > 0) norm_out<T, DROP>(a, key, row, vec, n, h[i], g[i], rstd, mg, mgh);
+      const int n = cols - column(i);
+      float va[8] = {};
+      if (add != nullptr) {
+        settle(r.add[i], n);
+        widen8f(r.add[i], va);
+      }
+      if (n > 0) norm_out<T, DROP>(a, key, row, column(i) / 8, n, h[i], g[i], va, r.rstd, mg, mgh);
     }
   }
   if (!a.sums) return;
@@ -173,7 +199,7 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBwdWaves : THR) void k_norm_bwd(N
   }
 }
 
-// Rows beyond the registers: dz by a workgroup per row, two reads of it; the
+// Rows beyond the registers (and below one vector): dz by a workgroup per row, two reads of it; the
 // weight gradients by k_norm_bwd_cols, a thread per 8 columns down a range of rows.
 template <typename T, bool DROP>
 __global__ __launch_bounds__(1024) void k_norm_bwd_long(NormBwdArgs a) {
@@ -195,7 +221,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_long(NormBwdArgs a) {
         load8(static_cast<const T*>(a.z) + at, n, z);
         load8(static_cast<const T*>(a.dy) + at, n, dy);
         load_param8<T>(a.weight, a.wf32, c, n, 1.0f, w);
-        norm_hg<T>(z, dy, w, mean, rstd, h, g);
+        norm_hg(z, dy, w, mean, rstd, h, g);
         if (pass == 0) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -203,7 +229,9 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_long(NormBwdArgs a) {
             sgh = __builtin_fmaf(g[j], h[j], sgh);
           }
         } else {
-          norm_out<T, DROP>(a, key, row, (int)(c / 8), n, h, g, rstd, mg, mgh);
+          float add[8] = {};
+          if (a.dz_add != nullptr) load8(static_cast<const T*>(a.dz_add) + at, n, add);
+          norm_out<T, DROP>(a, key, row, (int)(c / 8), n, h, g, add, rstd, mg, mgh);
         }
       }
       if (pass == 0) {
@@ -237,25 +265,41 @@ __global__ __launch_bounds__(256) void k_norm_bwd_cols(NormBwdArgs a) {
   store8(p + cols + c, n, db);
 }
 
-// dweight and dbias from `parts` partial sums of 2 * cols values: 32 columns and 32
-// ranges of the sums per workgroup, the ranges joined in LDS in order.
+// dweight and dbias from `nparts` partial sums of 2 * cols values: 32 columns (a cache
+// line of pairs) and 64 ranges of the sums per workgroup; the ranges are joined in LDS in a fixed order.
 __global__ __launch_bounds__(1024) void k_norm_parts(const float* parts, int nparts, int cols,
                                                      float* dweight, float* dbias) {
-  __shared__ float lds[32][33];
-  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+  typedef float pair_t __attribute__((ext_vector_type(2), aligned(4)));
+  __shared__ float lds[64][33];
+  const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
   const int64_t width = 2 * (int64_t)cols;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-  float s = 0.0f;
-  if (c < width)
-    for (int i = group; i < nparts; i += 32) s += parts[i * width + c];
-  lds[group][lane] = s;
+  const int64_t c = (int64_t)blockIdx.x * 32 + 2 * lane;
+  pair_t s = {0.0f, 0.0f};
+  if (c < width) {
+#pragma unroll 8
+    for (int i = group; i < nparts; i += 64)
+      s += *reinterpret_cast<const pair_t*>(parts + i * width + c);
+  }
+  lds[group][2 * lane] = s.x;
+  lds[group][2 * lane + 1] = s.y;
   __syncthreads();
-  if (group == 0 && c < width) {
+  // 32 columns x 8 ranges of 8, then the 8
+  float v = 0.0f;
+  const int col = threadIdx.x & 31, part = threadIdx.x >> 5;
+  if (part < 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += lds[part * 8 + i][col];
+  }
+  __syncthreads();
+  if (part < 8) lds[part][col] = v;
+  __syncthreads();
+  const int64_t o = (int64_t)blockIdx.x * 32 + col;
+  if (part == 0 && o < width) {
     float total = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) total += lds[i][lane];
-    if (c < cols) dweight[c] = total;
-    else dbias[c - cols] = total;
+    for (int i = 0; i < 8; ++i) total += lds[i][col];
+    if (o < cols) dweight[o] = total;
+    else dbias[o - cols] = total;
   }
 }
 
@@ -303,6 +347,7 @@ template <typename T, bool DROP>
 static int launch_bwd_width(const NormBwdArgs& a, float* dweight, float* dbias,
                             hipStream_t stream) {
   const int64_t nvec = ((int64_t)a.cols + 7) / 8;
+  if (a.cols < 8) return launch_bwd_long<T, DROP>(a, dweight, dbias, stream);
   if (nvec <= 64) return launch_bwd<T, 1, 64, DROP>(a, dweight, dbias, stream);
   if (nvec <= 128) return launch_bwd<T, 2, 64, DROP>(a, dweight, dbias, stream);
   if (nvec <= 256) return launch_bwd<T, 1, 256, DROP>(a, dweight, dbias, stream);

@@ -558,6 +558,26 @@ def gemm_bf16_quantize_fused(x: torch.Tensor, w: torch.Tensor, act: int = ACT_RE
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
+_F32, _I8 = torch.float32, torch.int8
+
+
+def _ptrs(*ts) -> list:
+    """_p of each tensor, with the checks that pass kept cheap (0.17 us a tensor, _p's 0.28)."""
+    device = None
+    out = []
+    for t in ts:
+        if t is None:
+            out.append(None)
+            continue
+        if device is None and t.is_cuda:
+            device = _current_device()
+        if t.get_device() == device and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            out.append(_p(t))          # raises
+    return out
+
+
 def _dtype(t: torch.Tensor, what: str) -> int:
     d = _DTYPES.get(t.dtype)
     if d is None:
@@ -567,14 +587,14 @@ def _dtype(t: torch.Tensor, what: str) -> int:
 
 def _like(t, x: torch.Tensor, what: str) -> None:
     """Refuse a tensor that is not of x's shape and type (None passes)."""
-    if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+    if t is not None and (t.dtype is not x.dtype or t.shape != x.shape):
         raise Fp8dpError(f"{what}: expected {x.dtype} {tuple(x.shape)}, got {t.dtype} "
                          f"{tuple(t.shape)}")
 
 
 def _floats(t, n: int, what: str) -> None:
     """Refuse a tensor that does not hold exactly n float32 values (None passes)."""
-    if t is not None and (t.dtype != torch.float32 or t.numel() != n):
+    if t is not None and (t.dtype is not _F32 or t.numel() != n):
         raise Fp8dpError(f"{what}: expected {n} float32 values, got {t.dtype} {tuple(t.shape)}")
 
 
@@ -584,11 +604,12 @@ def _params(ts, dtype: torch.dtype, n: int, what: str) -> int:
     for t in ts:
         if t is None:
             continue
-        if t.numel() != n or t.dtype not in (dtype, torch.float32) or got not in (None, t.dtype):
+        d = t.dtype
+        if t.numel() != n or (d is not dtype and d is not _F32) or (got is not None and d is not got):
             raise Fp8dpError(f"{what}: expected {n} values each, all {dtype} or all "
-                             f"float32, got {t.dtype} {tuple(t.shape)}")
-        got = t.dtype
-    return _DTYPES[got or dtype]
+                             f"float32, got {d} {tuple(t.shape)}")
+        got = d
+    return _DTYPES[dtype if got is None else got]
 
 
 def _rng(rng, what: str) -> None:
@@ -602,7 +623,7 @@ def _last(x: torch.Tensor, what: str) -> tuple:
     """(rows, cols) with cols the last dimension."""
     if x.dim() == 0:
         raise Fp8dpError(f"{what}: expected at least one dimension")
-    cols = x.shape[-1]
+    cols = x.size(-1)
     return (x.numel() // cols if cols else 0), cols
 
 
@@ -617,8 +638,9 @@ def layer_norm(x: torch.Tensor, weight, bias, eps: float, y: torch.Tensor, mean=
     wt = _params((weight, bias), x.dtype, cols, "layer_norm: weight, bias")
     _floats(mean, rows, "layer_norm: mean")
     _floats(rstd, rows, "layer_norm: rstd")
-    _check(lib().layer_norm(_p(x), _p(weight), _p(bias), rows, cols, dt, wt, eps, _p(y), _p(mean),
-                            _p(rstd), _stream(stream)), "layer_norm")
+    x, weight, bias, y, mean, rstd = _ptrs(x, weight, bias, y, mean, rstd)
+    _check(lib().layer_norm(x, weight, bias, rows, cols, dt, wt, eps, y, mean, rstd,
+                            _stream(stream)), "layer_norm")
 
 
 def layer_norm_backward(dy: torch.Tensor, z: torch.Tensor, weight, mean: torch.Tensor,
@@ -631,8 +653,10 @@ def layer_norm_backward(dy: torch.Tensor, z: torch.Tensor, weight, mean: torch.T
     dropout_add_layer_norm's p and rng."""
     dt = _dtype(z, "layer_norm_backward: z")
     rows, cols = _last(z, "layer_norm_backward: z")
-    for t, name in ((dy, "dy"), (dz, "dz"), (dz_add, "dz_add"), (dx, "dx")):
-        _like(t, z, f"layer_norm_backward: {name}")
+    _like(dy, z, "layer_norm_backward: dy")
+    _like(dz, z, "layer_norm_backward: dz")
+    _like(dz_add, z, "layer_norm_backward: dz_add")
+    _like(dx, z, "layer_norm_backward: dx")
     wt = _params((weight,), z.dtype, cols, "layer_norm_backward: weight")
     _floats(mean, rows, "layer_norm_backward: mean")
     _floats(rstd, rows, "layer_norm_backward: rstd")
@@ -644,9 +668,10 @@ def layer_norm_backward(dy: torch.Tensor, z: torch.Tensor, weight, mean: torch.T
             or workspace.numel() < 2 * min(rows, NORM_PARTS) * cols):
         raise Fp8dpError("layer_norm_backward: workspace needs 2 * min(rows, "
                          f"{NORM_PARTS}) * cols = {2 * min(rows, NORM_PARTS) * cols} float32")
-    _check(lib().layer_norm_backward(_p(dy), _p(z), _p(weight), _p(mean), _p(rstd), _p(dz_add),
-                                     rows, cols, dt, wt, p, _p(rng), _p(dz), _p(dx), _p(dweight),
-                                     _p(dbias), _p(workspace), _stream(stream)),
+    (dy, z, weight, mean, rstd, dz_add, rng, dz, dx, dweight, dbias, workspace) = _ptrs(
+        dy, z, weight, mean, rstd, dz_add, rng, dz, dx, dweight, dbias, workspace)
+    _check(lib().layer_norm_backward(dy, z, weight, mean, rstd, dz_add, rows, cols, dt, wt, p, rng,
+                                     dz, dx, dweight, dbias, workspace, _stream(stream)),
            "layer_norm_backward")
 
 
@@ -658,8 +683,9 @@ def dropout_add(x: torch.Tensor, residual, p: float, rng, out: torch.Tensor, str
     _like(residual, x, "dropout_add: residual")
     _like(out, x, "dropout_add: out")
     _rng(rng, "dropout_add")
-    _check(lib().dropout_add(_p(x), _p(residual), rows, cols, dt, p, _p(rng), _p(out),
-                             _stream(stream)), "dropout_add")
+    x, residual, rng, out = _ptrs(x, residual, rng, out)
+    _check(lib().dropout_add(x, residual, rows, cols, dt, p, rng, out, _stream(stream)),
+           "dropout_add")
 
 
 def dropout_add_layer_norm(x: torch.Tensor, residual, p: float, rng, weight, bias, eps: float,
@@ -668,19 +694,22 @@ def dropout_add_layer_norm(x: torch.Tensor, residual, p: float, rng, weight, bia
     """z = dropout_add(x, residual) and y = layer_norm(z) in one pass."""
     dt = _dtype(x, "dropout_add_layer_norm: x")
     rows, cols = _last(x, "dropout_add_layer_norm: x")
-    for t, name in ((residual, "residual"), (z, "z"), (y, "y")):
-        _like(t, x, f"dropout_add_layer_norm: {name}")
+    _like(residual, x, "dropout_add_layer_norm: residual")
+    _like(z, x, "dropout_add_layer_norm: z")
+    _like(y, x, "dropout_add_layer_norm: y")
     wt = _params((weight, bias), x.dtype, cols, "dropout_add_layer_norm: weight, bias")
     _floats(mean, rows, "dropout_add_layer_norm: mean")
     _floats(rstd, rows, "dropout_add_layer_norm: rstd")
     _rng(rng, "dropout_add_layer_norm")
-    _check(lib().dropout_add_layer_norm(_p(x), _p(residual), _p(weight), _p(bias), rows, cols, dt,
-                                        wt, p, _p(rng), eps, _p(z), _p(y), _p(mean), _p(rstd),
-                                        _stream(stream)), "dropout_add_layer_norm")
+    x, residual, weight, bias, rng, z, y, mean, rstd = _ptrs(x, residual, weight, bias, rng, z, y,
+                                                             mean, rstd)
+    _check(lib().dropout_add_layer_norm(x, residual, weight, bias, rows, cols, dt, wt, p, rng, eps,
+                                        z, y, mean, rstd, _stream(stream)),
+           "dropout_add_layer_norm")
 
 
 def _int8(t: torch.Tensor, what: str) -> None:
-    if t.dtype != torch.int8:
+    if t.dtype is not _I8:
         raise Fp8dpError(f"{what}: expected int8 codes, got {t.dtype}")
 
 
@@ -693,8 +722,8 @@ def quantize_int8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=
     if q.shape != x.shape:
         raise Fp8dpError("quantize_int8: q must have x's shape")
     _floats(scale, rows, "quantize_int8: scale")
-    _check(lib().quantize_int8(_p(x), rows, cols, dt, _p(q), _p(scale), _stream(stream)),
-           "quantize_int8")
+    x, q, scale = _ptrs(x, q, scale)
+    _check(lib().quantize_int8(x, rows, cols, dt, q, scale, _stream(stream)), "quantize_int8")
 
 
 def layer_norm_quantize_int8(x: torch.Tensor, weight, bias, eps: float, q: torch.Tensor,
@@ -710,23 +739,25 @@ def layer_norm_quantize_int8(x: torch.Tensor, weight, bias, eps: float, q: torch
     if q.shape != x.shape:
         raise Fp8dpError("layer_norm_quantize_int8: q must have x's shape")
     _floats(scale, rows, "layer_norm_quantize_int8: scale")
-    _check(lib().layer_norm_quantize_int8(_p(x), _p(residual), _p(weight), _p(bias), rows, cols,
-                                          dt, wt, eps, _p(z), _p(q), _p(scale), _stream(stream)),
-           "layer_norm_quantize_int8")
+    x, residual, weight, bias, z, q, scale = _ptrs(x, residual, weight, bias, z, q, scale)
+    _check(lib().layer_norm_quantize_int8(x, residual, weight, bias, rows, cols, dt, wt, eps, z, q,
+                                          scale, _stream(stream)), "layer_norm_quantize_int8")
 
 
 def _int8_operands(name: str, a: torch.Tensor, b: torch.Tensor, b_scale, y: torch.Tensor,
                    bias) -> tuple:
     """(M, N, K, y's type, bias' type) of a product a [..., K] x b [N, K] -> y [..., N]."""
-    _int8(b, f"{name}: weight")
-    yt = _dtype(y, f"{name}: y")
-    M, K = _last(a, f"{name}: a")
-    if b.dim() != 2 or b.shape[1] != K or y.dim() == 0 or y.shape[:-1] != a.shape[:-1] or \
-            y.shape[-1] != b.shape[0]:
+    _int8(b, "weight")
+    yt = _dtype(y, "y")
+    M, K = _last(a, name)
+    if b.dim() != 2 or y.dim() != a.dim():
         raise Fp8dpError(f"{name}: shape mismatch")
-    N = b.shape[0]
-    _floats(b_scale, N, f"{name}: weight scale")
-    return M, N, K, yt, _params((bias,), y.dtype, N, f"{name}: bias")
+    N, k = b.shape
+    if k != K or y.size(-1) != N or y.numel() != M * N or \
+            (a.dim() > 2 and y.shape[:-1] != a.shape[:-1]):
+        raise Fp8dpError(f"{name}: shape mismatch")
+    _floats(b_scale, N, "weight scale")
+    return M, N, K, yt, yt if bias is None else _params((bias,), y.dtype, N, "bias")
 
 
 def int8_gemm(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: torch.Tensor,
@@ -738,8 +769,9 @@ def int8_gemm(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: 
     M, N, K, yt, bt = _int8_operands("int8_gemm", a, b, b_scale, y, bias)
     _floats(a_scale, M, "int8_gemm: a_scale")
     room = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().int8_gemm(_p(a), _p(b), M, N, K, _p(a_scale), _p(b_scale), _p(bias), yt, bt,
-                           _p(y), _p(workspace), room, _stream(stream)), "int8_gemm")
+    a, b, a_scale, b_scale, bias, y, workspace = _ptrs(a, b, a_scale, b_scale, bias, y, workspace)
+    _check(lib().int8_gemm(a, b, M, N, K, a_scale, b_scale, bias, yt, bt, y, workspace, room,
+                           _stream(stream)), "int8_gemm")
 
 
 def int8_linear_workspace(M: int, K: int) -> int:
@@ -752,11 +784,12 @@ def int8_linear(x: torch.Tensor, w8: torch.Tensor, w_scale: torch.Tensor, y: tor
     """y [..., N] = x [..., K] W^T + bias with x cast to INT8 per token (quantize_int8) and W
     given as codes w8 [N, K] and w_scale [N]; x and y of one type.  workspace: at least
     int8_linear_workspace(M, K) bytes; up to 16 MiB beyond serve the split of K."""
-    if _dtype(x, "int8_linear: x") != _DTYPES.get(y.dtype):
+    if x.dtype is not y.dtype:
         raise Fp8dpError(f"int8_linear: y must be of x's type, {x.dtype}, got {y.dtype}")
     M, N, K, yt, bt = _int8_operands("int8_linear", x, w8, w_scale, y, bias)
-    _check(lib().int8_linear(_p(x), _p(w8), _p(w_scale), _p(bias), M, N, K, yt, bt, _p(y),
-                             _p(workspace), workspace.numel() * workspace.element_size(),
+    room = workspace.numel() * workspace.element_size()
+    x, w8, w_scale, bias, y, workspace = _ptrs(x, w8, w_scale, bias, y, workspace)
+    _check(lib().int8_linear(x, w8, w_scale, bias, M, N, K, yt, bt, y, workspace, room,
                              _stream(stream)), "int8_linear")
 
 

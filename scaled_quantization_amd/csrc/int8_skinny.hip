@@ -85,12 +85,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_i8_skinny(I8Args g, const T* x) 
     auto absmax = [](const Raw8<T>& raw, uint32_t m) {
       float w[8];
       widen8f(raw, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t b = __float_as_uint(w[j]) & 0x7FFFFFFFu;
-        m = b > m ? b : m;
-      }
-      return m;
+      return magnitude8(w, m);
     };
     // the rule of item i's token, once all parts of its largest magnitude are in `top`
     auto rule = [&](int i, bool& plain) {

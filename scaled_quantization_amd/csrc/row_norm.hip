@@ -31,158 +31,132 @@ struct RowArgs {
   float* scale;
 };
 
-// T: element type.  NV vectors of 8 per thread in registers (0: a loop over longer
-// rows, and rows of less than 8).  THR threads per row.  DROP: apply the mask.  NORM / QUANT:
-// the norm, the cast.  Without both, z (or out) is all there is to write.
+// T: element type.  NV: vectors of 8 per thread, ceil(cols / 8 / THR).  THR: threads per row.
+// DROP: apply the mask.  NORM / QUANT: the norm, the cast.  Without both, z (or out) is
+// all there is to write.
+//
+// A wave costs 4 cycles an instruction on its SIMD, so rows that come from cache are
+// bound by the instructions per element, not by memory: the parameters are widened
+// once for all rows of a wave, the masks of the last vector are kept in registers, and
+// the next row is loaded while one is in hand (the last one loads itself again).
 template <typename T, int NV, int THR, bool DROP, bool NORM, bool QUANT>
-__global__ __launch_bounds__(THR < 256 ? 256 : THR) void k_row(RowArgs a) {
-  constexpr int RPB = THR < 256 ? 256 / THR : 1;   // rows per workgroup
-  constexpr bool REG = NV > 0;
-  constexpr int HELD = REG ? NV : 1;
+__global__ __launch_bounds__(THR == 64 ? 256 : THR) void k_row(RowArgs a) {
+  constexpr int RPB = THR == 64 ? 4 : 1;   // rows per workgroup
   constexpr int WAVES = THR / 64;
   __shared__ float scratch[THR > 64 ? 2 * 3 * WAVES : 1];
   const int t = THR > 64 ? (int)threadIdx.x : (int)(threadIdx.x & 63);
   const int sub = THR > 64 ? 0 : (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cols = a.cols;
-  const int nvec = (int)(((QUANT ? a.ldq : (int64_t)cols) + 7) / 8);
-  const int steps = REG ? NV : (nvec + THR - 1) / THR;
-  const float fcols = (float)cols;
+  const bool ragged = cols % 8 != 0;
+  const float inv_cols = 1.0f / (float)cols;
   const T* const x = static_cast<const T*>(a.x);
   const T* const residual = static_cast<const T*>(a.residual);
   DropKey key = {};
   if constexpr (DROP) key = drop_key(a.rng);
+  auto column = [&](int i) { return (i * THR + t) * 8; };
+  const int n_last = cols - column(NV - 1);
+  auto count = [&](int i) { return i < NV - 1 ? 8 : n_last; };   // elements of vector i
+  const Mask8 mask(n_last);
+
+  struct Row {
+    Raw8<T> x[NV], r[NV];
+  };
+  auto load = [&](int64_t row, Row& o) {
+    const int64_t base = row * cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) o.x[i] = load_row(x + base, column(i), cols);
+    if (residual != nullptr) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) o.r[i] = load_row(residual + base, column(i), cols);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB, begin = (int64_t)blockIdx.x * RPB + sub;
+  if (begin >= a.rows) return;   // (whole waves, or with THR > 64 whole workgroups)
+  Row next;
+  load(begin, next);
+
+  float g[NORM ? NV : 1][8], b[NORM ? NV : 1][8];
+  if constexpr (NORM) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      load_param8<T>(a.weight, a.wf32, column(i), count(i), 1.0f, g[i]);
+      load_param8<T>(a.bias, a.wf32, column(i), count(i), 0.0f, b[i]);
+    }
+    mask.clear(g[NV - 1]);   // (NULL parameters fill all 8)
+    mask.clear(b[NV - 1]);
+  }
 
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < a.rows;
-       row += (int64_t)gridDim.x * RPB, turn ^= 1) {
+  for (int64_t row = begin; row < a.rows; row += step, turn ^= 1) {
     float* const sc = scratch + (THR > 64 ? turn * 3 * WAVES : 0);
     const int64_t base = row * cols;
-    auto column = [&](int i) { return (i * THR + t) * 8; };
-    float v[HELD][8];
+    const Row now = next;
+    load(row + step < a.rows ? row + step : row, next);
+
+    float v[NV][8];
     float sum = 0.0f;
     uint32_t top = 0;
-
-    // one vector of the row: mask, residual sum, z, and its part of the first statistic
-    auto begin = [&](int i, float* w, const float* r) {
-      const int c = column(i), n = cols - c;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float* const w = v[i];
+      Raw8<T> raw = now.x[i];
+      if (i == NV - 1) {
+        settle(raw, n_last, ragged);
+        mask.clear_empty(raw);
+      }
+      widen8f(raw, w);
       if constexpr (DROP) drop8(key, a.rule, (uint32_t)(i * THR + t), (uint32_t)row, w);
       if (residual != nullptr) {
+        float r[8];
+        raw = now.r[i];
+        if (i == NV - 1) {
+          settle(raw, n_last, ragged);
+          mask.clear_empty(raw);
+        }
+        widen8f(raw, r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] += r[j];
       }
       if (a.z != nullptr) {
-        through8<T>(w);
-        store8(static_cast<T*>(a.z) + base + c, n, w);
+        const Raw8<T> out = round8(w, T{});
+        store_row(static_cast<T*>(a.z) + base + column(i), count(i), out);
+        widen8f(out, w);
       }
       if constexpr (NORM) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum += w[j];
       } else if constexpr (QUANT) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t b = __float_as_uint(w[j]) & 0x7FFFFFFFu;
-          top = b > top ? b : top;
-        }
-      }
-    };
-    // parameters of a vector: held as loaded (issued ahead of the row), or loaded at their use
-    RawParam pw[HELD], pb[HELD];
-    auto params = [&](int i, int n, float* g, float* b) {
-      if constexpr (REG) {
-        widen_param<T>(pw[i], a.weight, a.wf32, n, 1.0f, g);
-        widen_param<T>(pb[i], a.bias, a.wf32, n, 0.0f, b);
-      } else {
-        load_param8<T>(a.weight, a.wf32, column(i), n, 1.0f, g);
-        load_param8<T>(a.bias, a.wf32, column(i), n, 0.0f, b);
-      }
-    };
-    if constexpr (REG) {
-      // every load of the row first, without a branch, then the arithmetic
-      Raw8<T> rx[NV], rr[NV];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) rx[i] = load_row(x + base, column(i), cols);
-      if (residual != nullptr) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) rr[i] = load_row(residual + base, column(i), cols);
-      }
-      if constexpr (NORM) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          pw[i] = load_param<T>(a.weight, a.wf32, column(i), cols);
-          pb[i] = load_param<T>(a.bias, a.wf32, column(i), cols);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int n = cols - column(i);
-        float r[8] = {};
-        settle(rx[i], n);
-        widen8f(rx[i], v[i]);
-        if (residual != nullptr) {
-          settle(rr[i], n);
-          widen8f(rr[i], r);
-        }
-        begin(i, v[i], r);
-      }
-    } else {
-      for (int i = 0; i < steps; ++i) {
-        const int c = column(i), n = cols - c;
-        float r[8] = {};
-        load8(x + base + c, n, v[0]);
-        if (residual != nullptr) load8(residual + base + c, n, r);
-        begin(i, v[0], r);
+        top = magnitude8(w, top);
       }
     }
-    // f(i, values): from the registers, or read again
-    auto each = [&](auto&& f) {
-      if constexpr (REG) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) f(i, v[i]);
-      } else {
-        const T* const from = a.z != nullptr ? static_cast<const T*>(a.z) : x;
-        for (int i = 0; i < steps; ++i) {
-          load8(from + base + column(i), cols - column(i), v[0]);
-          f(i, v[0]);
-        }
-      }
-    };
 
-    float mean = 0.0f, rstd = 0.0f;
     if constexpr (NORM) {
-      mean = row_sum<THR>(sum, sc) / fcols;
+      const float mean = row_sum<THR>(sum, sc) * inv_cols;
       float sq = 0.0f;
-      each([&](int i, float* w) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] -= mean;
-        zero_from8(cols - column(i), w);
+      for (int i = 0; i < NV; ++i) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(w[j], w[j], sq);
-      });
-      const float var = row_sum<THR>(sq, sc + WAVES) / fcols;
-      rstd = 1.0f / __fsqrt_rn(var + a.eps);
+        for (int j = 0; j < 8; ++j) v[i][j] -= mean;
+        if (i == NV - 1) mask.clear(v[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(v[i][j], v[i][j], sq);
+      }
+      const float rstd = rsqrtf(row_sum<THR>(sq, sc + WAVES) * inv_cols + a.eps);
       if (t == 0) {
         if (a.mean != nullptr) a.mean[row] = mean;
         if (a.rstd != nullptr) a.rstd[row] = rstd;
       }
-      // in registers the row is now x - mean; read again it is x
-      each([&](int i, float* w) {
-        const int c = column(i), n = cols - c;
-        float g[8], b[8];
-        params(i, n, g, b);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          w[j] = __builtin_fmaf((REG ? w[j] : w[j] - mean) * rstd, g[j], b[j]);
+      for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = __builtin_fmaf(v[i][j] * rstd, g[i][j], b[i][j]);
         if constexpr (QUANT) {
-          zero_from8(n, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t m = __float_as_uint(w[j]) & 0x7FFFFFFFu;
-            top = m > top ? m : top;
-          }
+          if (i == NV - 1) mask.clear(v[i]);   // (a NaN row's padding too)
+          top = magnitude8(v[i], top);
         } else {
-          store8(static_cast<T*>(a.y) + base + c, n, w);
+          store_row(static_cast<T*>(a.y) + base + column(i), count(i), round8(v[i], T{}));
         }
-      });
+      }
     }
 
     if constexpr (QUANT) {
@@ -193,31 +167,138 @@ __global__ __launch_bounds__(THR < 256 ? 256 : THR) void k_row(RowArgs a) {
         a.scale[row] = plain ? __uint_as_float(top) / 127.0f
                              : (top == 0 ? 0.0f : __builtin_nanf(""));
       int8_t* const q = a.q + row * a.ldq;
-      each([&](int i, float* w) {
-        const int c = column(i), n = cols - c;
-        if constexpr (NORM && !REG) {
-          float g[8], b[8];
-          params(i, n, g, b);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) w[j] = __builtin_fmaf((w[j] - mean) * rstd, g[j], b[j]);
-          zero_from8(n, w);
-        }
+      for (int i = 0; i < NV; ++i) {
+        const int c = column(i);
         uint2 code = {0u, 0u};
-        if (plain) code = codes8<NORM || sizeof(T) == 4>(w, s);
-        const int64_t room = a.ldq - c;
-        store_codes8(q + c, room < 8 ? (int)room : 8, code);
-      });
+        if (plain) code = codes8<!NORM && sizeof(T) == 4>(v[i], s);
+        // rows of q may be padded by up to 15 bytes of zeros
+        if (i < NV - 1) store_codes8(q + c, 8, code);
+        else store_codes8(q + c, a.ldq - c < 8 ? (int)(a.ldq - c) : 8, code);
+      }
     }
   }
 }
 
+// Rows of more than 16384 elements, or less than 8: a loop that reads the row
+// again for each statistic and for the output.
+template <typename T, int THR, bool DROP, bool NORM, bool QUANT>
+__global__ __launch_bounds__(THR == 64 ? 256 : THR) void k_row_loop(RowArgs a) {
+  constexpr int RPB = THR == 64 ? 4 : 1;
+  constexpr int WAVES = THR / 64;
+  __shared__ float scratch[THR > 64 ? 2 * 3 * WAVES : 1];
+  const int t = THR > 64 ? (int)threadIdx.x : (int)(threadIdx.x & 63);
+  const int sub = THR > 64 ? 0 : (int)(threadIdx.x >> 6);
+  const int cols = a.cols;
+  const int wide = (int)(QUANT ? a.ldq : (int64_t)cols);
+  const float inv_cols = 1.0f / (float)cols;
+  const T* const x = static_cast<const T*>(a.x);
+  const T* const residual = static_cast<const T*>(a.residual);
+  DropKey key = {};
+  if constexpr (DROP) key = drop_key(a.rng);
+
+  int turn = 0;
+  for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < a.rows;
+       row += (int64_t)gridDim.x * RPB, turn ^= 1) {
+    float* const sc = scratch + (THR > 64 ? turn * 3 * WAVES : 0);
+    const int64_t base = row * cols;
+    const T* const again = (a.z != nullptr ? static_cast<const T*>(a.z) : x) + base;
+    float w[8], sum = 0.0f, mean = 0.0f, rstd = 0.0f;
+    uint32_t top = 0;
+    auto normed = [&](int c) {
+      float g[8], b[8];
+      load8(again + c, cols - c, w);
+      load_param8<T>(a.weight, a.wf32, c, cols - c, 1.0f, g);
+      load_param8<T>(a.bias, a.wf32, c, cols - c, 0.0f, b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = __builtin_fmaf((w[j] - mean) * rstd, g[j], b[j]);
+      zero_from8(cols - c, w);
+    };
+    for (int c = t * 8; c < cols; c += THR * 8) {
+      const int n = cols - c;
+      load8(x + base + c, n, w);
+      if constexpr (DROP) drop8(key, a.rule, (uint32_t)(c / 8), (uint32_t)row, w);
+      if (residual != nullptr) {
+        float r[8];
+        load8(residual + base + c, n, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] += r[j];
+      }
+      if (a.z != nullptr) {
+        through8<T>(w);
+        store8(static_cast<T*>(a.z) + base + c, n, w);
+      }
+      if constexpr (NORM) {
+        zero_from8(n, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += w[j];
+      } else if constexpr (QUANT) {
+        top = magnitude8(w, top);
+      }
+    }
+    if constexpr (NORM) {
+      mean = row_sum<THR>(sum, sc) * inv_cols;
+      float sq = 0.0f;
+      for (int c = t * 8; c < cols; c += THR * 8) {
+        load8(again + c, cols - c, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] -= mean;
+        zero_from8(cols - c, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(w[j], w[j], sq);
+      }
+      rstd = rsqrtf(row_sum<THR>(sq, sc + WAVES) * inv_cols + a.eps);
+      if (t == 0) {
+        if (a.mean != nullptr) a.mean[row] = mean;
+        if (a.rstd != nullptr) a.rstd[row] = rstd;
+      }
+      for (int c = t * 8; c < cols; c += THR * 8) {
+        normed(c);
+        if constexpr (QUANT) top = magnitude8(w, top);
+        else store8(static_cast<T*>(a.y) + base + c, cols - c, w);
+      }
+    }
+    if constexpr (QUANT) {
+      top = row_umax<THR>(top, reinterpret_cast<uint32_t*>(sc) + 2 * WAVES);
+      const bool plain = top != 0 && top < 0x7F800000u;
+      const RowScale s = row_scale(plain ? top : 0x3F800000u);
+      if (t == 0)
+        a.scale[row] = plain ? __uint_as_float(top) / 127.0f
+                             : (top == 0 ? 0.0f : __builtin_nanf(""));
+      for (int c = t * 8; c < wide; c += THR * 8) {
+        if constexpr (NORM) normed(c);
+        else load8(again + c, cols - c, w);
+        uint2 code = {0u, 0u};
+        if (plain) code = codes8<!NORM && sizeof(T) == 4>(w, s);
+        store_codes8(a.q + row * a.ldq + c, wide - c, code);
+      }
+    }
+  }
+}
+
+// Waves per compute unit that the grid is made for.  Tensors that the caches hold (512 MB
+// moved in all: the last-level cache has 256 MB) do best with few waves that walk many rows,
+// which spares them the parameters and masks; streams from memory with many
+// short ones, whose reads and writes the scheduler keeps apart.  Measured, 16 against
+// 256 waves: layer norm 16384 x 768 10.1 / 13.3 us, dropout + residual + norm 30001 x 1600 75 / 95;
+// layer norm 65536 x 4096 205 / 177, with dropout and residual 443 / 385.  The norm
+// with the cast is bound by its instructions either way (65536 x 4096: 168 / 178).
+constexpr int64_t kRowStreamBytes = (int64_t)512 << 20;
+
 template <typename T, int NV, int THR, bool DROP, bool NORM, bool QUANT>
 static int launch_row(const RowArgs& a, const char* what, hipStream_t stream) {
-  constexpr int RPB = THR < 256 ? 256 / THR : 1;
+  constexpr int RPB = THR == 64 ? 4 : 1, BLOCK = THR == 64 ? 256 : THR;
   const int64_t need = (a.rows + RPB - 1) / RPB;
-  const unsigned grid = grid_for(need * 256, 256, 64);
-  hipLaunchKernelGGL((k_row<T, NV, THR, DROP, NORM, QUANT>), dim3(grid),
-                     dim3(THR < 256 ? 256 : THR), 0, stream, a);
+  const int64_t per = sizeof(T) * (1 + (a.residual != nullptr) + (a.z != nullptr) + (a.y != nullptr)) +
+                      (QUANT ? 1 : 0);
+  const bool streams = a.rows * a.cols * per > kRowStreamBytes && !(NORM && QUANT);
+  const unsigned grid = grid_for(need * BLOCK, BLOCK, std::max(1, (streams ? 256 : 16) * 64 / BLOCK));
+  if constexpr (NV > 0)
+    hipLaunchKernelGGL((k_row<T, NV, THR, DROP, NORM, QUANT>), dim3(grid), dim3(BLOCK), 0, stream,
+                       a);
+  else
+    hipLaunchKernelGGL((k_row_loop<T, THR, DROP, NORM, QUANT>), dim3(grid), dim3(BLOCK), 0, stream,
+                       a);
   return check_launch(what);
 }
 
@@ -228,9 +309,11 @@ static int launch_width(const RowArgs& a, const char* what, hipStream_t stream) 
   if (a.cols < 8) return launch_row<T, 0, 64, DROP, NORM, QUANT>(a, what, stream);
   if (nvec <= 64) return launch_row<T, 1, 64, DROP, NORM, QUANT>(a, what, stream);
   if (nvec <= 128) return launch_row<T, 2, 64, DROP, NORM, QUANT>(a, what, stream);
+  if (nvec <= 192) return launch_row<T, 3, 64, DROP, NORM, QUANT>(a, what, stream);
   if (nvec <= 256) return launch_row<T, 4, 64, DROP, NORM, QUANT>(a, what, stream);
   if (nvec <= 512) return launch_row<T, 2, 256, DROP, NORM, QUANT>(a, what, stream);
-  if (nvec <= 1024) return launch_row<T, 4, 256, DROP, NORM, QUANT>(a, what, stream);
+  if (nvec <= 768) return launch_row<T, 3, 256, DROP, NORM, QUANT>(a, what, stream);
+  if (nvec <= 1024) return launch_row<T, 1, 1024, DROP, NORM, QUANT>(a, what, stream);
   if (nvec <= 2048) return launch_row<T, 2, 1024, DROP, NORM, QUANT>(a, what, stream);
   return launch_row<T, 0, 1024, DROP, NORM, QUANT>(a, what, stream);
 }

@@ -77,7 +77,7 @@ __device__ __forceinline__ void row_sum2(float& x, float& y, float* scratch) {
   }
 }
 
-constexpr int kBwdWaves = 8;   // waves of a workgroup whose waves own rows
+constexpr int kBwdWaves = 4;   // waves of a workgroup whose waves own rows
 
 template <typename T, int NV, int THR, bool DROP>
 __global__ __launch_bounds__(THR == 64 ? 64 * kBwdWaves : THR) void k_norm_bwd(NormBwdArgs a) {
@@ -86,12 +86,16 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBwdWaves : THR) void k_norm_bwd(N
   const int t = THR > 64 ? (int)threadIdx.x : (int)(threadIdx.x & 63);
   const int sub = THR > 64 ? 0 : (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cols = a.cols;
-  const float fcols = (float)cols;
+  const bool ragged = cols % 8 != 0;
+  const float inv_cols = 1.0f / (float)cols;
   const T *const z = static_cast<const T*>(a.z), *const dy = static_cast<const T*>(a.dy),
           *const add = static_cast<const T*>(a.dz_add);
   DropKey key = {};
   if constexpr (DROP) key = drop_key(a.rng);
   auto column = [&](int i) { return (i * THR + t) * 8; };
+
+  const int n_last = cols - column(NV - 1);
+  const Mask8 mask(n_last);
 
   // the row in hand and the next one, still as loaded: a row's loads have a whole
   // row of arithmetic to arrive
@@ -100,19 +104,19 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBwdWaves : THR) void k_norm_bwd(N
     float mean, rstd;
   };
   auto load = [&](int64_t row, Row& r) {
-    const int64_t base = (row < a.rows ? row : a.rows - 1) * cols;
+    const int64_t base = row * cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       r.z[i] = load_row(z + base, column(i), cols);
       r.dy[i] = load_row(dy + base, column(i), cols);
       if (add != nullptr) r.add[i] = load_row(add + base, column(i), cols);
     }
-    r.mean = a.mean[row < a.rows ? row : a.rows - 1];
-    r.rstd = a.rstd[row < a.rows ? row : a.rows - 1];
+    r.mean = a.mean[row];
+    r.rstd = a.rstd[row];
   };
   const int64_t step = (int64_t)gridDim.x * RPB, first = (int64_t)blockIdx.x * RPB + sub;
   Row next;
-  load(first, next);
+  load(first < a.rows ? first : a.rows - 1, next);   // (the grid has no more workgroups than rows; a spare wave loads the last)
 
   float w[NV][8], dw[NV][8], db[NV][8];
 #pragma unroll
@@ -124,17 +128,19 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBwdWaves : THR) void k_norm_bwd(N
 
   int turn = 0;
   for (int64_t row = first; row < a.rows; row += step, turn ^= 1) {
-    Row r = next;
-    load(row + step, next);
+    const Row r = next;
+    load(row + step < a.rows ? row + step : row, next);
     float h[NV][8], g[NV][8], sg = 0.0f, sgh = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int n = cols - column(i);
       float vz[8], vd[8];
-      settle(r.z[i], n);
-      settle(r.dy[i], n);
-      widen8f(r.z[i], vz);
-      widen8f(r.dy[i], vd);
+      Raw8<T> raw = r.z[i];
+      if (i == NV - 1) settle(raw, n_last, ragged);
+      widen8f(raw, vz);
+      raw = r.dy[i];
+      if (i == NV - 1) settle(raw, n_last, ragged);
+      widen8f(raw, vd);
+      if (i == NV - 1) mask.clear(vd);
       norm_hg(vz, vd, w[i], r.mean, r.rstd, h[i], g[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -145,16 +151,17 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBwdWaves : THR) void k_norm_bwd(N
       }
     }
     row_sum2<THR>(sg, sgh, lds + (THR > 64 ? turn * 2 * (THR / 64) : 0));
-    const float mg = sg / fcols, mgh = sgh / fcols;
+    const float mg = sg * inv_cols, mgh = sgh * inv_cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int n = cols - column(i);
+      const int n = i < NV - 1 ? 8 : n_last;
       float va[8] = {};
       if (add != nullptr) {
-        settle(r.add[i], n);
-        widen8f(r.add[i], va);
+        Raw8<T> raw = r.add[i];
+        if (i == NV - 1) settle(raw, n_last, ragged);
+        widen8f(raw, va);
       }
-      if (n > 0) norm_out<T, DROP>(a, key, row, column(i) / 8, n, h[i], g[i], va, r.rstd, mg, mgh);
+      if (i < NV - 1 || n > 0) norm_out<T, DROP>(a, key, row, column(i) / 8, n, h[i], g[i], va, r.rstd, mg, mgh);
     }
   }
   if (!a.sums) return;
@@ -205,7 +212,7 @@ template <typename T, bool DROP>
 __global__ __launch_bounds__(1024) void k_norm_bwd_long(NormBwdArgs a) {
   __shared__ float lds[2 * 2 * 16];
   const int t = threadIdx.x, cols = a.cols;
-  const float fcols = (float)cols;
+  const float inv_cols = 1.0f / (float)cols;
   DropKey key = {};
   if constexpr (DROP) key = drop_key(a.rng);
   int turn = 0;
@@ -236,8 +243,8 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_long(NormBwdArgs a) {
       }
       if (pass == 0) {
         row_sum2<1024>(sg, sgh, lds + turn * 32);
-        mg = sg / fcols;
-        mgh = sgh / fcols;
+        mg = sg * inv_cols;
+        mgh = sgh * inv_cols;
       }
     }
   }
@@ -313,10 +320,16 @@ static int launch_parts(const NormBwdArgs& a, int nparts, float* dweight, float*
 template <typename T, int NV, int THR, bool DROP>
 static int launch_bwd(const NormBwdArgs& a, float* dweight, float* dbias, hipStream_t stream) {
   constexpr int RPB = THR == 64 ? kBwdWaves : 1;
-  int64_t grid = (a.rows + RPB - 1) / RPB;
-  const int64_t cap = std::min<int64_t>(FP8DP_NORM_PARTS,
-                                        (int64_t)num_cus() * std::max(1, 1024 / (RPB * THR)));
-  if (grid > cap) grid = cap;
+  // as many workgroups as the device holds at once: all walk the same number of rows
+  static const int resident = [] {
+    int n = 0;
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, (k_norm_bwd<T, NV, THR, DROP>), RPB * THR,
+                                                     0) != hipSuccess || n < 1)
+      n = 1;
+    return n;
+  }();
+  const int64_t cap = std::min<int64_t>(FP8DP_NORM_PARTS, (int64_t)num_cus() * resident);
+  const int64_t grid = std::min<int64_t>((a.rows + RPB - 1) / RPB, cap);
   hipLaunchKernelGGL((k_norm_bwd<T, NV, THR, DROP>), dim3((unsigned)grid), dim3(RPB * THR), 0,
                      stream, a);
   const int rc = check_launch("layer_norm_backward");

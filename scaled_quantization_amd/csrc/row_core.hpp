@@ -163,6 +163,18 @@ __device__ __forceinline__ void store8(T* p, int n, const float v[8]) {
       if (j < n) p[j] = from_f32<T>(v[j]);
   }
 }
+// Element c of a row whose address is the same for the wave: the address stays in scalar
+// registers and the offset is one 32-bit register.
+template <typename T>
+__device__ __forceinline__ const T* element(const T* row, int c) {
+  return reinterpret_cast<const T*>(reinterpret_cast<const char*>(row) +
+                                    (uint32_t)c * (uint32_t)sizeof(T));
+}
+template <typename T>
+__device__ __forceinline__ T* element(T* row, int c) {
+  return reinterpret_cast<T*>(reinterpret_cast<char*>(row) + (uint32_t)c * (uint32_t)sizeof(T));
+}
+
 // n elements of a vector already rounded.
 template <typename T>
 __device__ __forceinline__ void store_row(T* p, int n, const Raw8<T>& r) {
@@ -184,7 +196,7 @@ __device__ __forceinline__ void store_row(T* p, int n, const Raw8<T>& r) {
 // its mask, kept over all rows, clears the rest.
 template <typename T>
 __device__ __forceinline__ Raw8<T> load_row(const T* row, int c, int cols) {
-  return load_raw8(row + (c < cols - 8 ? c : cols - 8));
+  return load_raw8(element(row, c < cols - 8 ? c : cols - 8));
 }
 __device__ __forceinline__ u32x4_e_t shift_down(u32x4_e_t w, int s) {   // by s bits, s > 0
   uint64_t lo = (uint64_t)w[1] << 32 | w[0], hi = (uint64_t)w[3] << 32 | w[2];

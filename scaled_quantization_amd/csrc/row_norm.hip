@@ -119,7 +119,7 @@ __global__ __launch_bounds__(THR == 64 ? 256 : THR) void k_row(RowArgs a) {
       }
       if (a.z != nullptr) {
         const Raw8<T> out = round8(w, T{});
-        store_row(static_cast<T*>(a.z) + base + column(i), count(i), out);
+        store_row(element(static_cast<T*>(a.z) + base, column(i)), count(i), out);
         widen8f(out, w);
       }
       if constexpr (NORM) {
@@ -154,7 +154,7 @@ __global__ __launch_bounds__(THR == 64 ? 256 : THR) void k_row(RowArgs a) {
           if (i == NV - 1) mask.clear(v[i]);   // (a NaN row's padding too)
           top = magnitude8(v[i], top);
         } else {
-          store_row(static_cast<T*>(a.y) + base + column(i), count(i), round8(v[i], T{}));
+          store_row(element(static_cast<T*>(a.y) + base, column(i)), count(i), round8(v[i], T{}));
         }
       }
     }
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(THR == 64 ? 256 : THR) void k_row(RowArgs a) {
         uint2 code = {0u, 0u};
         if (plain) code = codes8<!NORM && sizeof(T) == 4>(v[i], s);
         // rows of q may be padded by up to 15 bytes of zeros
-        if (i < NV - 1) store_codes8(q + c, 8, code);
+        if (i < NV - 1) store_codes8(element(q, c), 8, code);
         else store_codes8(q + c, a.ldq - c < 8 ? (int)(a.ldq - c) : 8, code);
       }
     }

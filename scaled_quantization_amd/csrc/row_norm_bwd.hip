@@ -42,7 +42,7 @@ template <typename T, bool DROP>
 __device__ __forceinline__ void norm_out(const NormBwdArgs& a, const DropKey& key, int64_t row,
                                          int vec, int n, const float h[8], const float g[8],
                                          const float add[8], float rstd, float mg, float mgh) {
-  const int64_t at = row * a.cols + (int64_t)vec * 8;
+  const int64_t base = row * a.cols;
   float d[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) d[j] = rstd * (g[j] - mg - h[j] * mgh);
@@ -50,10 +50,10 @@ __device__ __forceinline__ void norm_out(const NormBwdArgs& a, const DropKey& ke
 #pragma unroll
     for (int j = 0; j < 8; ++j) d[j] += add[j];
   }
-  store8(static_cast<T*>(a.dz) + at, n, d);
+  store8(element(static_cast<T*>(a.dz) + base, vec * 8), n, d);
   if (a.dx != nullptr) {
     if constexpr (DROP) drop8(key, a.rule, (uint32_t)vec, (uint32_t)row, d);
-    store8(static_cast<T*>(a.dx) + at, n, d);
+    store8(element(static_cast<T*>(a.dx) + base, vec * 8), n, d);
   }
 }
 
@@ -116,7 +116,7 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBwdWaves : THR) void k_norm_bwd(N
   };
   const int64_t step = (int64_t)gridDim.x * RPB, first = (int64_t)blockIdx.x * RPB + sub;
   Row next;
-  load(first < a.rows ? first : a.rows - 1, next);   // (the grid has no more workgroups than rows; a spare wave loads the last)
+  load(first < a.rows ? first : a.rows - 1, next);   // (a spare wave loads the last row)
 
   float w[NV][8], dw[NV][8], db[NV][8];
 #pragma unroll
@@ -130,23 +130,30 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBwdWaves : THR) void k_norm_bwd(N
   for (int64_t row = first; row < a.rows; row += step, turn ^= 1) {
     const Row r = next;
     load(row + step < a.rows ? row + step : row, next);
-    float h[NV][8], g[NV][8], sg = 0.0f, sgh = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float vz[8], vd[8];
+    float sg = 0.0f, sgh = 0.0f;
+    // h and g of vector i (the compiler keeps them over the reduction where registers allow)
+    auto make = [&](int i, float* h, float* g, float* vd) {
+      float vz[8];
       Raw8<T> raw = r.z[i];
       if (i == NV - 1) settle(raw, n_last, ragged);
       widen8f(raw, vz);
       raw = r.dy[i];
-      if (i == NV - 1) settle(raw, n_last, ragged);
+      if (i == NV - 1) {
+        settle(raw, n_last, ragged);
+        mask.clear_empty(raw);
+      }
       widen8f(raw, vd);
-      if (i == NV - 1) mask.clear(vd);
-      norm_hg(vz, vd, w[i], r.mean, r.rstd, h[i], g[i]);
+      norm_hg(vz, vd, w[i], r.mean, r.rstd, h, g);
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float h[8], g[8], vd[8];
+      make(i, h, g, vd);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        sg += g[i][j];
-        sgh = __builtin_fmaf(g[i][j], h[i][j], sgh);
-        dw[i][j] = __builtin_fmaf(vd[j], h[i][j], dw[i][j]);
+        sg += g[j];
+        sgh = __builtin_fmaf(g[j], h[j], sgh);
+        dw[i][j] = __builtin_fmaf(vd[j], h[j], dw[i][j]);
         db[i][j] += vd[j];
       }
     }
@@ -161,7 +168,10 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBwdWaves : THR) void k_norm_bwd(N
         if (i == NV - 1) settle(raw, n_last, ragged);
         widen8f(raw, va);
       }
-      if (i < NV - 1 || n > 0) norm_out<T, DROP>(a, key, row, column(i) / 8, n, h[i], g[i], va, r.rstd, mg, mgh);
+      float h[8], g[8], vd[8];
+      make(i, h, g, vd);
+      if (i < NV - 1 || n > 0)
+        norm_out<T, DROP>(a, key, row, column(i) / 8, n, h, g, va, r.rstd, mg, mgh);
     }
   }
   if (!a.sums) return;
@@ -366,7 +376,7 @@ static int launch_bwd_width(const NormBwdArgs& a, float* dweight, float* dbias,
   if (nvec <= 256) return launch_bwd<T, 1, 256, DROP>(a, dweight, dbias, stream);
   if (nvec <= 512) return launch_bwd<T, 2, 256, DROP>(a, dweight, dbias, stream);
   if (nvec <= 1024) return launch_bwd<T, 1, 1024, DROP>(a, dweight, dbias, stream);
-  if (nvec <= 2048) return launch_bwd<T, 2, 1024, DROP>(a, dweight, dbias, stream);
+  // two vectors per thread of 1024 spill (128 registers a thread): 4096 x 16384 took 243 us, this 157
   return launch_bwd_long<T, DROP>(a, dweight, dbias, stream);
 }
 

@@ -23,6 +23,14 @@ struct I8Args {
   void* y;
 };
 
+// Whether the rows of both operands start at multiples of 16 bytes and K is one too.
+inline bool rows16(const I8Args& g) {
+  return g.K % 16 == 0 && g.lda % 16 == 0 && g.ldb % 16 == 0 && aligned16(g.a) && aligned16(g.b);
+}
+
+// What chunks past K are copied from.
+__device__ const u32x4_t kZeroChunk = {0, 0, 0, 0};
+
 // 16 bytes at any byte address.
 __device__ __forceinline__ v4i_t load16(const int8_t* p) {
   const u32x4_b_t v = *reinterpret_cast<const u32x4_b_t*>(p);

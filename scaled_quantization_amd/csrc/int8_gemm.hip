@@ -109,8 +109,8 @@ static int launch_i8(const char* what, const I8Args& g, void* workspace, int64_t
 
 static int dispatch_i8(const char* what, fp8dp_dtype yt, const I8Args& g, void* workspace,
                        int64_t workspace_bytes, hipStream_t stream) {
-  if (g.M <= 64 && g.K >= 128) return skinny_i8(what, yt, g, nullptr, stream);
-  if (tile_takes(g)) return tile_i8(what, yt, g, stream);
+  if (g.M <= kFewTokens) return skinny_i8(what, yt, g, nullptr, stream);
+  if (rows16(g)) return tile_i8(what, yt, g, stream);
   if (yt == FP8DP_BF16) return launch_i8<bf16_t>(what, g, workspace, workspace_bytes, stream);
   if (yt == FP8DP_F16) return launch_i8<f16_t>(what, g, workspace, workspace_bytes, stream);
   return launch_i8<float>(what, g, workspace, workspace_bytes, stream);
@@ -183,17 +183,16 @@ extern "C" int int8_linear(const void* x, const int8_t* w8, const float* w_scale
   if (!aligned_to(x, dtype_size(dt)) || !aligned_to(w_scale, 4) || !aligned_to(y, dtype_size(dt)) ||
       !aligned_to(bias, dtype_size(bt)))
     return bad_align(what);
-  if (skinny_casts(M, K)) {
-    const I8Args g = {nullptr, w8, (int)M, (int)N, (int)K, K, K, nullptr, w_scale, bias,
-                      bt == FP8DP_F32, y};
-    return skinny_i8(what, dt, g, x, stream);
-  }
+  I8Args g = {nullptr, w8, (int)M, (int)N, (int)K, K, K, nullptr, w_scale, bias, bt == FP8DP_F32, y};
+  if (skinny_casts(g, x, (int)dtype_size(dt))) return skinny_i8(what, dt, g, x, stream);
   const int64_t ld = padded_k(K);
   int8_t* const q = static_cast<int8_t*>(workspace);
   float* const scale = reinterpret_cast<float*>(q + M * ld);
   rc = quantize_rows(what, x, M, K, dt, q, ld, scale, stream);
   if (rc) return rc;
-  const I8Args g = {q, w8, (int)M, (int)N, (int)K, ld, K, scale, w_scale, bias, bt == FP8DP_F32, y};
+  g.a = q;
+  g.lda = ld;
+  g.sa = scale;
   return dispatch_i8(what, dt, g, static_cast<uint8_t*>(workspace) + need, workspace_bytes - need,
                      stream);
 }

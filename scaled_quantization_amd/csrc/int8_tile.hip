@@ -22,8 +22,6 @@ namespace fp8dp {
 
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-__device__ const u32x4_t kZeroChunk = {0, 0, 0, 0};
-
 // Lane i's 16 bytes at base + off[i] land at l + 16 i; as copy16_to_lds, with
 // the wave's base in scalar registers.
 __device__ __forceinline__ void copy16_to_lds_at(const int8_t* base, uint32_t off, uint8_t* l) {
@@ -223,10 +221,6 @@ static int tile_type(const char* what, const I8Args& g, hipStream_t stream) {
   if (tiles(256, 256) >= cus) return launch_tile<T, 4, 2, 2, 4, 2>(what, g, stream);
   if (tiles(128, 128) >= cus) return launch_tile<T, 2, 2, 2, 2, 2>(what, g, stream);
   return launch_tile<T, 2, 2, 1, 1, 4>(what, g, stream);
-}
-
-bool tile_takes(const I8Args& g) {
-  return g.K % 16 == 0 && g.lda % 16 == 0 && g.ldb % 16 == 0 && aligned16(g.a) && aligned16(g.b);
 }
 
 int tile_i8(const char* what, fp8dp_dtype yt, const I8Args& g, hipStream_t stream) {

@@ -4,8 +4,7 @@
 
 namespace fp8dp {
 
-// Whether rows start and end at multiples of 16 bytes.
-bool tile_takes(const I8Args& g);
+// For operands that rows16() accepts.
 int tile_i8(const char* what, fp8dp_dtype yt, const I8Args& g, hipStream_t stream);
 
 }  // namespace fp8dp

@@ -118,8 +118,9 @@ int layer_norm_quantize_int8(const void* x, const void* residual, const void* we
    the sum exact in 32-bit integers.  a: [M x K], b: [N x K] int8 (all of
    -128 .. 127), bias: [N] of type bt, which is yt or FP8DP_F32, or NULL; y: [M x N] of type yt.
    workspace: scratch that lets the library split K over workgroups when there
-   are few tiles of y; NULL or any size is fine (16 MiB is all it ever uses).
-   Calls that share a workspace must not overlap in time.
+   are few tiles of y (16 MiB is all that takes), and copy operands whose rows do not start
+   at multiples of 16 bytes into rows that do (K rounded up to 16 bytes a row of each); NULL
+   or any size is fine.  Calls that share a workspace must not overlap in time.
    Errors: EINVAL for a NULL operand, scale or y, M or N outside 1 .. 2^30, K
    outside 1 .. FP8DP_INT8_MAX_K, unknown types, a misaligned pointer
    (workspace: 16 bytes), or workspace_bytes < 0. */
@@ -129,7 +130,7 @@ int int8_gemm(const int8_t* a, const int8_t* b, int64_t M, int64_t N, int64_t K,
               hipStream_t stream);
 
 /* Least workspace of int8_linear, in bytes: the tokens' codes, their rows padded to a
-   multiple of 16 bytes, and their scales.  What is beyond it serves int8_gemm's split. */
+   multiple of 16 bytes, and their scales.  What is beyond it serves int8_gemm as its workspace. */
 int64_t int8_linear_workspace(int64_t M, int64_t K);
 
 /* quantize_int8 of x [M x K] (type dt) and int8_gemm with w8 [N x K] and w_scale

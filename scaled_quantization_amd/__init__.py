@@ -764,7 +764,8 @@ def int8_gemm(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: 
               y: torch.Tensor, bias=None, workspace=None, stream=None) -> None:
     """y [..., N] = (a [..., K] b [N, K]^T) a_scale[row] b_scale[channel] + bias, int8
     codes summed exactly; y bfloat16, float16 or float32, bias of y's type or float32.
-    workspace (any contiguous tensor, 16-byte aligned) lets K be split where y is small."""
+    workspace (any contiguous tensor, 16-byte aligned) lets K be split where y is small, and
+    operands with unaligned rows be copied where y is large."""
     _int8(a, "int8_gemm: a")
     M, N, K, yt, bt = _int8_operands("int8_gemm", a, b, b_scale, y, bias)
     _floats(a_scale, M, "int8_gemm: a_scale")
@@ -783,7 +784,7 @@ def int8_linear(x: torch.Tensor, w8: torch.Tensor, w_scale: torch.Tensor, y: tor
                 workspace: torch.Tensor, bias=None, stream=None) -> None:
     """y [..., N] = x [..., K] W^T + bias with x cast to INT8 per token (quantize_int8) and W
     given as codes w8 [N, K] and w_scale [N]; x and y of one type.  workspace: at least
-    int8_linear_workspace(M, K) bytes; up to 16 MiB beyond serve the split of K."""
+    int8_linear_workspace(M, K) bytes; what is beyond serves as int8_gemm's workspace."""
     if x.dtype is not y.dtype:
         raise Fp8dpError(f"int8_linear: y must be of x's type, {x.dtype}, got {y.dtype}")
     M, N, K, yt, bt = _int8_operands("int8_linear", x, w8, w_scale, y, bias)

@@ -129,4 +129,58 @@ __device__ __forceinline__ void widen_bias4(const I8Args& g, const RawCols4& r, 
   }
 }
 
+// Epilogue of a wave's TM x TN tiles of 32 x 32 at rows m0, columns n0.  In such a tile the lane
+// holds token lane % 32 and register r channel 8 (r / 4) + 4 (lane / 32) + r % 4: stored
+// from there, a row gets 8 bytes at a time.  The wave turns its tiles in its own 32 x 32 TN words
+// of LDS, 32 tokens at a time as binary32 (sum times token scale), and reads them back
+// with 8 consecutive channels per lane, whose scales and bias it then holds for all rows,
+// and whole cache lines per row to store.  16-byte chunks are swizzled by row against
+// bank conflicts.
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+template <typename T, int TM, int TN>
+__device__ __forceinline__ void turn_out(const I8Args& g, const v16i_t (&acc)[TM][TN],
+                                         uint8_t* part, int m0, int n0, int lane) {
+  constexpr int CW = TN * 32, LPR = CW / 8, RPI = 64 / LPR;   // columns, lanes per row, rows per step
+  const int frow = lane & 31, fhalf = lane >> 5;
+  auto at = [&](int r, int c) {   // byte of chunk c (4 channels) of row r
+    return r * CW * 4 + ((c ^ (TN == 1 ? (r >> 1) & 7 : r & 15)) << 4);
+  };
+  const int n = n0 + (lane % LPR) * 8;
+  const RawCols4 c0 = load_cols4<T>(g, n), c1 = load_cols4<T>(g, n + 4);
+  float sa[TM];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int m = m0 + 32 * i + frow;
+    sa[i] = g.sa[m < g.M ? m : g.M - 1];
+  }
+  float bias[8];
+  widen_bias4<T>(g, c0, bias);
+  widen_bias4<T>(g, c1, bias + 4);
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f32x4_t v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = (float)acc[i][j][4 * q + r] * sa[i];
+        *reinterpret_cast<f32x4_t*>(part + at(frow, j * 8 + 2 * q + fhalf)) = v;
+      }
+#pragma unroll
+    for (int s = 0; s < 32 / RPI; ++s) {
+      const int r = s * RPI + lane / LPR, m = m0 + 32 * i + r, c = (lane % LPR) * 2;
+      const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(part + at(r, c));
+      const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(part + at(r, c + 1));
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[k] = lo[k] * c0.sb[k] + bias[k];
+        v[k + 4] = hi[k] * c1.sb[k] + bias[k + 4];
+      }
+      if (m < g.M && n < g.N) store8(static_cast<T*>(g.y) + (int64_t)m * g.N + n, g.N - n, v);
+    }
+  }
+}
+
 }  // namespace fp8dp

@@ -20,8 +20,6 @@
 
 namespace fp8dp {
 
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-
 // Lane i's 16 bytes at base + off[i] land at l + 16 i; as copy16_to_lds, with
 // the wave's base in scalar registers.
 __device__ __forceinline__ void copy16_to_lds_at(const int8_t* base, uint32_t off, uint8_t* l) {
@@ -148,54 +146,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_i8_tile(I8Args g) {
     multiply(fa1, fb1);
   }
 
-  // Epilogue.  In a 32 x 32 tile the lane holds token lane % 32 and register r channel
-  // 8 (r / 4) + 4 (lane / 32) + r % 4: stored from there, a row gets 8 bytes at a time.  Each
-  // wave turns its tiles in its own part of the ring, 32 tokens at a time as binary32 (sum times
-  // token scale), and reads them back with 8 consecutive channels per lane, whose scales and
-  // bias it then holds for all rows, and whole cache lines per row to store.
-  // 16-byte chunks are swizzled by row against bank conflicts.
-  constexpr int CW = TN * 32, LPR = CW / 8, RPI = 64 / LPR;   // columns, lanes per row, rows per step
-  static_assert(W * 32 * CW * 4 <= S * SLOT, "the waves' parts fit the ring");
-  uint8_t* const part = lds + wave * 32 * CW * 4;
-  auto at = [&](int r, int c) {   // byte of chunk c (4 channels) of row r
-    return r * CW * 4 + ((c ^ (TN == 1 ? (r >> 1) & 7 : r & 15)) << 4);
-  };
-  const int n = n0 + wc + (lane % LPR) * 8;
-  const RawCols4 c0 = load_cols4<T>(g, n), c1 = load_cols4<T>(g, n + 4);
-  float sa[TM];
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int m = m0 + wr + 32 * i + frow;
-    sa[i] = g.sa[m < g.M ? m : g.M - 1];
-  }
-  float bias[8];
-  widen_bias4<T>(g, c0, bias);
-  widen_bias4<T>(g, c1, bias + 4);
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        f32x4_t v;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = (float)acc[i][j][4 * q + r] * sa[i];
-        *reinterpret_cast<f32x4_t*>(part + at(frow, j * 8 + 2 * q + fhalf)) = v;
-      }
-#pragma unroll
-    for (int s = 0; s < 32 / RPI; ++s) {
-      const int r = s * RPI + lane / LPR, m = m0 + wr + 32 * i + r, c = (lane % LPR) * 2;
-      const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(part + at(r, c));
-      const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(part + at(r, c + 1));
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[k] = lo[k] * c0.sb[k] + bias[k];
-        v[k + 4] = hi[k] * c1.sb[k] + bias[k + 4];
-      }
-      if (m < g.M && n < g.N) store8(static_cast<T*>(g.y) + (int64_t)m * g.N + n, g.N - n, v);
-    }
-  }
+  static_assert(W * 32 * TN * 128 <= S * SLOT, "the waves' parts fit the ring");
+  turn_out<T, TM, TN>(g, acc, lds + wave * 32 * TN * 128, m0 + wr, n0 + wc, lane);
 }
 
 template <typename T, int WM, int WN, int TM, int TN, int S>
@@ -211,22 +163,15 @@ static int launch_tile(const char* what, const I8Args& g, hipStream_t stream) {
   return check_launch(what);
 }
 
-template <typename T>
-static int tile_type(const char* what, const I8Args& g, hipStream_t stream) {
-  // the largest tile that still gives every compute unit one
-  auto tiles = [&](int bm, int bn) {
-    return (((int64_t)g.M + bm - 1) / bm) * (((int64_t)g.N + bn - 1) / bn);
+int tile_i8(const char* what, fp8dp_dtype yt, const I8Args& g, bool wide, hipStream_t stream) {
+  auto run = [&](auto t) -> int {
+    using T = decltype(t);
+    return wide ? launch_tile<T, 4, 2, 2, 4, 2>(what, g, stream)
+                : launch_tile<T, 2, 2, 2, 2, 2>(what, g, stream);
   };
-  const int64_t cus = num_cus();
-  if (tiles(256, 256) >= cus) return launch_tile<T, 4, 2, 2, 4, 2>(what, g, stream);
-  if (tiles(128, 128) >= cus) return launch_tile<T, 2, 2, 2, 2, 2>(what, g, stream);
-  return launch_tile<T, 2, 2, 1, 1, 4>(what, g, stream);
-}
-
-int tile_i8(const char* what, fp8dp_dtype yt, const I8Args& g, hipStream_t stream) {
-  if (yt == FP8DP_BF16) return tile_type<bf16_t>(what, g, stream);
-  if (yt == FP8DP_F16) return tile_type<f16_t>(what, g, stream);
-  return tile_type<float>(what, g, stream);
+  if (yt == FP8DP_BF16) return run(bf16_t{});
+  if (yt == FP8DP_F16) return run(f16_t{});
+  return run(float{});
 }
 
 }  // namespace fp8dp

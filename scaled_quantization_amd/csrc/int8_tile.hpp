@@ -4,7 +4,7 @@
 
 namespace fp8dp {
 
-// For operands that rows16() accepts.
-int tile_i8(const char* what, fp8dp_dtype yt, const I8Args& g, hipStream_t stream);
+// For operands that rows16() accepts; tiles of 256 x 256 (wide) or 128 x 128 outputs.
+int tile_i8(const char* what, fp8dp_dtype yt, const I8Args& g, bool wide, hipStream_t stream);
 
 }  // namespace fp8dp

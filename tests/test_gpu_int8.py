@@ -156,6 +156,33 @@ def test_int8_gemm_largest_sums(M, N, K):
     check_product(y, a, b, sa, sb, None, torch.float32, "all -128")
 
 
+def test_int8_product_with_copied_operands():
+    # rows at any byte and enough work: with a workspace both operands are copied to aligned rows
+    # (int8_linear: the weight alone), without one they are not; the sums are the same
+    M, N, K = 4200, 2100, 1901
+    a, b, sa, sb = operands(M, N, K, 9)
+    dev = [torch.from_numpy(v).to(DEV) for v in (a, b, sa, sb)]
+    ys = []
+    for room in (0, (M + N) * 1904, (M + N) * 1904 - 1, 1 << 25):
+        y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+        sq.int8_gemm(*dev, y, None, torch.full((room,), 0x33, dtype=torch.uint8, device=DEV) if room else None)
+        ys.append(y)
+    assert all(torch.equal(ys[0], y) for y in ys[1:])
+    rows = np.array([0, 1, 63, 64, 255, 256, 2047, 4095, 4096, 4198, 4199])
+    check_product(ys[0], a, b, sa, sb, None, torch.bfloat16, "copied", rows)
+    x = draw((M, K), torch.bfloat16, 1)
+    need = sq.int8_linear_workspace(M, K)
+    out = []
+    for room in (need, need + N * 1904):
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=DEV)
+        sq.int8_linear(x.to(DEV), dev[1], dev[3], y, torch.full((room,), 0x33, dtype=torch.uint8, device=DEV))
+        out.append(y)
+    assert torch.equal(*out)
+    q, s = OB.quantize_int8(f64(x)[rows])
+    check_product(out[0][torch.from_numpy(rows).to(DEV)], q, b, s.astype(np.float32), sb, None, torch.bfloat16,
+                  "linear, copied")
+
+
 @pytest.mark.parametrize("off", [1, 4, 8])
 def test_int8_gemm_operands_that_start_at_any_byte(off):
     for M, N, K in ((33, 70, 256), (300, 260, 512), (3, 64, 1024)):

@@ -18,6 +18,8 @@
 #include "int8_core.hpp"
 #include "int8_tile.hpp"
 
+#include <type_traits>
+
 namespace fp8dp {
 
 // Lane i's 16 bytes at base + off[i] land at l + 16 i; as copy16_to_lds, with
@@ -41,7 +43,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_i8_tile(I8Args g) {
   const int tiles_n = (g.N + BN - 1) / BN;
   const int ntiles = ((g.M + BM - 1) / BM) * tiles_n;
   const int tile = tile_of_block(blockIdx.x, ntiles);
-  const int m0 = (tile / tiles_n) * BM, n0 = (tile % tiles_n) * BN;
+  // bands 4 tiles wide: the 32 tiles that an XCD has in hand are 8 x 4, whose operands are 12
+  // tiles in all, not 2 x 16
+  const int tiles_m = (g.M + BM - 1) / BM, band = tile / (4 * tiles_m);
+  const int in_band = tile - band * 4 * tiles_m, wide = tiles_n - band * 4 < 4 ? tiles_n - band * 4 : 4;
+  const int m0 = in_band / wide * BM, n0 = (band * 4 + in_band % wide) * BN;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = (wave / WN) * TM * 32, wc = (wave % WN) * TN * 32;
@@ -91,22 +97,28 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_i8_tile(I8Args g) {
     }
   };
 
-  const int frow = lane & 31, fhalf = lane >> 5;
-  // 64 bytes of K (half h of a stage) as two 32-byte steps
-  auto load_frags = [&](int kt, int h, v4i_t (&fa)[2][TM], v4i_t (&fb)[2][TN]) {
-    const uint8_t* const sA = lds + (kt % S) * SLOT;
-    const uint8_t* const sB = sA + ASZ;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int c = h * 4 + q * 2 + fhalf;
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-        fa[q][i] = *reinterpret_cast<const v4i_t*>(sA + swz(wr + 32 * i + frow, c));
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-        fb[q][j] = *reinterpret_cast<const v4i_t*>(sB + swz(wc + 32 * j + frow, c));
-    }
+  // one copy of a whole stage
+  auto copy_one = [&](auto C, const int8_t* a, const int8_t* b, uint8_t* base) {
+    constexpr int c = decltype(C)::value;
+    if constexpr (c < LA) copy16_to_lds_at(a, offA[c], base + c * W * 1024);
+    else copy16_to_lds_at(b, offB[c - LA], base + ASZ + (c - LA) * W * 1024);
   };
+
+  // fragments of 64 bytes of K (half h of a stage) in two 32-byte steps: one read of the 2 (TM + TN)
+  struct Frags {
+    v4i_t a[2][TM], b[2][TN];
+  };
+  const int frow = lane & 31, fhalf = lane >> 5;
+  auto read_one = [&](auto X, const uint8_t* slot, int h, Frags& f) {
+    constexpr int x = decltype(X)::value, q = x / (TM + TN), i = x % (TM + TN);
+    const int c = h * 4 + q * 2 + fhalf;
+    if constexpr (i < TM)
+      f.a[q][i] = *reinterpret_cast<const v4i_t*>(slot + swz(wr + 32 * i + frow, c));
+    else
+      f.b[q][i - TM] =
+          *reinterpret_cast<const v4i_t*>(slot + ASZ + swz(wc + 32 * (i - TM) + frow, c));
+  };
+  constexpr int READS = 2 * (TM + TN), PRODUCTS = 2 * TM * TN;
   v16i_t acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -114,14 +126,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_i8_tile(I8Args g) {
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
-  auto multiply = [&](const v4i_t (&fa)[2][TM], const v4i_t (&fb)[2][TN]) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[q][j], fa[q][i], acc[i][j], 0, 0, 0);
+  // the products of a half stage, with between(0), between(1), ... after one each: reads and
+  // copies issue while a product runs, instead of before the first one
+  auto multiply = [&](const Frags& f, auto&& between) {
+    static_for<PRODUCTS>([&](auto X) {
+      constexpr int x = decltype(X)::value, q = x / (TM * TN), i = x / TN % TM, j = x % TN;
+      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.b[q][j], f.a[q][i], acc[i][j], 0, 0, 0);
+      between(X);
+      __builtin_amdgcn_sched_barrier(0);
+    });
   };
 
 #pragma unroll
@@ -131,20 +144,44 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_i8_tile(I8Args g) {
   else wait_vmcnt<0>();
   stage_barrier();
 
-  v4i_t fa0[2][TM], fb0[2][TN], fa1[2][TM], fb1[2][TN];
-  load_frags(0, 0, fa0, fb0);
-  for (int kt = 0; kt < KT; ++kt) {
-    load_frags(kt, 1, fa1, fb1);
-    multiply(fa0, fb0);
-    __builtin_amdgcn_sched_barrier(0);
+  static_assert(READS <= PRODUCTS + 8 && NCOPY <= PRODUCTS, "what fits between the products");
+  constexpr int EACH = (READS + PRODUCTS - 1) / PRODUCTS;   // reads after a product
+  Frags f0, f1;
+  static_for<READS>([&](auto X) { read_one(X, lds, 0, f0); });
+  // one stage; COPY: the stage S later is whole and copied between the products (else, near the end of K,
+  // ahead of them); NEXT: there is a next stage
+  auto stage = [&](int kt, auto COPY, auto NEXT) {
+    constexpr bool copy = decltype(COPY)::value, next = decltype(NEXT)::value;
+    const uint8_t* const slot = lds + (kt % S) * SLOT;
+    const uint8_t* const after = lds + ((kt + 1) % S) * SLOT;
+    auto reads = [&](auto X, const uint8_t* from, int h, Frags& f) {
+      static_for<EACH>([&](auto E) {
+        constexpr int x = decltype(X)::value * EACH + decltype(E)::value;
+        if constexpr (x < READS) read_one(std::integral_constant<int, x>{}, from, h, f);
+      });
+    };
+    multiply(f0, [&](auto X) { reads(X, slot, 1, f1); });
     __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's reads of stage kt are done
-    if (kt + S - 1 < KT) wait_vmcnt<(S - 2) * NCOPY>();   // its copies of stage kt + 1 have landed
+    // its copies of stage kt + 1 have landed
+    if (copy || kt + S - 1 < KT) wait_vmcnt<(S - 2) * NCOPY>();
     else wait_vmcnt<0>();
     stage_barrier();
-    if (kt + S < KT) issue(kt + S);
-    if (kt + 1 < KT) load_frags(kt + 1, 0, fa0, fb0);
-    multiply(fa1, fb1);
-  }
+    if constexpr (!copy) {
+      if (kt + S < KT) issue(kt + S);
+    }
+    const int k0 = (kt + S) * kBK;
+    uint8_t* const base = lds + (kt % S) * SLOT + wave * 1024;
+    multiply(f1, [&](auto X) {
+      if constexpr (next) reads(X, after, 0, f0);
+      if constexpr (copy && decltype(X)::value < NCOPY) copy_one(X, baseA + k0, baseB + k0, base);
+    });
+  };
+  using yes = std::true_type;
+  using no = std::false_type;
+  int kt = 0;
+  for (; (kt + S + 1) * kBK <= g.K; ++kt) stage(kt, yes{}, yes{});
+  for (; kt + 1 < KT; ++kt) stage(kt, no{}, yes{});
+  stage(kt, no{}, no{});
 
   static_assert(W * 32 * TN * 128 <= S * SLOT, "the waves' parts fit the ring");
   turn_out<T, TM, TN>(g, acc, lds + wave * 32 * TN * 128, m0 + wr, n0 + wc, lane);

@@ -43,17 +43,17 @@ template <> __device__ __forceinline__ f16_t from_f32<f16_t>(float v) {
 }
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 
-template <typename T>
+template <bool STREAM = false, typename T>
 __device__ __forceinline__ Raw8<T> load_raw8(const T* p) {
   Raw8<T> r;
-  r.w = *reinterpret_cast<const u32x4_e_t*>(p);
-  return r;
-}
-template <>
-__device__ __forceinline__ Raw8<float> load_raw8<float>(const float* p) {
-  Raw8<float> r;
-  r.lo = *reinterpret_cast<const f32x4_e_t*>(p);
-  r.hi = *reinterpret_cast<const f32x4_e_t*>(p + 4);
+  if constexpr (sizeof(T) == 4) {
+    const f32x4_e_t* const q = reinterpret_cast<const f32x4_e_t*>(p);
+    r.lo = STREAM ? __builtin_nontemporal_load(q) : q[0];
+    r.hi = STREAM ? __builtin_nontemporal_load(q + 1) : q[1];
+  } else {
+    const u32x4_e_t* const q = reinterpret_cast<const u32x4_e_t*>(p);
+    r.w = STREAM ? __builtin_nontemporal_load(q) : q[0];
+  }
   return r;
 }
 
@@ -194,9 +194,10 @@ __device__ __forceinline__ void store_row(T* p, int n, const Raw8<T>& r) {
 // (i = NV - 1) can be cut or empty: settle() moves its n elements to the front
 // once they have arrived (`ragged`: cols is no multiple of 8, the same for all threads), and
 // its mask, kept over all rows, clears the rest.
-template <typename T>
+// STREAM: not to be kept in the caches.
+template <bool STREAM = false, typename T>
 __device__ __forceinline__ Raw8<T> load_row(const T* row, int c, int cols) {
-  return load_raw8(element(row, c < cols - 8 ? c : cols - 8));
+  return load_raw8<STREAM>(element(row, c < cols - 8 ? c : cols - 8));
 }
 __device__ __forceinline__ u32x4_e_t shift_down(u32x4_e_t w, int s) {   // by s bits, s > 0
   uint64_t lo = (uint64_t)w[1] << 32 | w[0], hi = (uint64_t)w[3] << 32 | w[2];

@@ -561,21 +561,19 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _F32, _I8 = torch.float32, torch.int8
 
 
+def _device() -> int:
+    """The current device; -2, which no tensor is on, where there is none."""
+    try:
+        return _current_device()
+    except RuntimeError:
+        return -2
+
+
 def _ptrs(*ts) -> list:
-    """_p of each tensor, with the checks that pass kept cheap (0.17 us a tensor, _p's 0.28)."""
-    device = None
-    out = []
-    for t in ts:
-        if t is None:
-            out.append(None)
-            continue
-        if device is None and t.is_cuda:
-            device = _current_device()
-        if t.get_device() == device and t.is_contiguous():
-            out.append(t.data_ptr())
-        else:
-            out.append(_p(t))          # raises
-    return out
+    """_p of each tensor, with the checks that pass kept cheap."""
+    device = _device()
+    return [None if t is None else
+            t.data_ptr() if t.get_device() == device and t.is_contiguous() else _p(t) for t in ts]
 
 
 def _dtype(t: torch.Tensor, what: str) -> int:
@@ -585,10 +583,10 @@ def _dtype(t: torch.Tensor, what: str) -> int:
     return d
 
 
-def _like(t, x: torch.Tensor, what: str) -> None:
-    """Refuse a tensor that is not of x's shape and type (None passes)."""
-    if t is not None and (t.dtype is not x.dtype or t.shape != x.shape):
-        raise Fp8dpError(f"{what}: expected {x.dtype} {tuple(x.shape)}, got {t.dtype} "
+def _like(t, dtype: torch.dtype, shape: torch.Size, what: str) -> None:
+    """Refuse a tensor that is not of this type and shape (None passes)."""
+    if t is not None and (t.dtype is not dtype or t.shape != shape):
+        raise Fp8dpError(f"{what}: expected {dtype} {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)}")
 
 
@@ -619,11 +617,13 @@ def _rng(rng, what: str) -> None:
                          f"{rng.dtype} {tuple(rng.shape)}")
 
 
-def _last(x: torch.Tensor, what: str) -> tuple:
-    """(rows, cols) with cols the last dimension."""
-    if x.dim() == 0:
+def _last(x: torch.Tensor, shape: torch.Size, what: str) -> tuple:
+    """(rows, cols) of a tensor of this shape, cols its last dimension."""
+    if len(shape) == 2:
+        return shape
+    if not shape:
         raise Fp8dpError(f"{what}: expected at least one dimension")
-    cols = x.size(-1)
+    cols = shape[-1]
     return (x.numel() // cols if cols else 0), cols
 
 
@@ -633,8 +633,9 @@ def layer_norm(x: torch.Tensor, weight, bias, eps: float, y: torch.Tensor, mean=
     float32, weight and bias of the same type or float32 (None: ones, zeros);
     mean, rstd: float32, one value per row, for the backward pass."""
     dt = _dtype(x, "layer_norm: x")
-    rows, cols = _last(x, "layer_norm: x")
-    _like(y, x, "layer_norm: y")
+    x_shape = x.shape
+    rows, cols = _last(x, x_shape, "layer_norm: x")
+    _like(y, x.dtype, x_shape, "layer_norm: y")
     wt = _params((weight, bias), x.dtype, cols, "layer_norm: weight, bias")
     _floats(mean, rows, "layer_norm: mean")
     _floats(rstd, rows, "layer_norm: rstd")
@@ -652,11 +653,12 @@ def layer_norm_backward(dy: torch.Tensor, z: torch.Tensor, weight, mean: torch.T
     of 2 * min(rows, NORM_PARTS) * cols values), and dx, dz through the mask of
     dropout_add_layer_norm's p and rng."""
     dt = _dtype(z, "layer_norm_backward: z")
-    rows, cols = _last(z, "layer_norm_backward: z")
-    _like(dy, z, "layer_norm_backward: dy")
-    _like(dz, z, "layer_norm_backward: dz")
-    _like(dz_add, z, "layer_norm_backward: dz_add")
-    _like(dx, z, "layer_norm_backward: dx")
+    z_shape = z.shape
+    rows, cols = _last(z, z_shape, "layer_norm_backward: z")
+    _like(dy, z.dtype, z_shape, "layer_norm_backward: dy")
+    _like(dz, z.dtype, z_shape, "layer_norm_backward: dz")
+    _like(dz_add, z.dtype, z_shape, "layer_norm_backward: dz_add")
+    _like(dx, z.dtype, z_shape, "layer_norm_backward: dx")
     wt = _params((weight,), z.dtype, cols, "layer_norm_backward: weight")
     _floats(mean, rows, "layer_norm_backward: mean")
     _floats(rstd, rows, "layer_norm_backward: rstd")
@@ -679,9 +681,10 @@ def dropout_add(x: torch.Tensor, residual, p: float, rng, out: torch.Tensor, str
     """out = residual + keep x / (1 - p) (residual None: no sum); rng: [seed, offset], two
     64-bit integers on the device.  The same call on the gradient is the backward pass."""
     dt = _dtype(x, "dropout_add: x")
-    rows, cols = _last(x, "dropout_add: x")
-    _like(residual, x, "dropout_add: residual")
-    _like(out, x, "dropout_add: out")
+    x_shape = x.shape
+    rows, cols = _last(x, x_shape, "dropout_add: x")
+    _like(residual, x.dtype, x_shape, "dropout_add: residual")
+    _like(out, x.dtype, x_shape, "dropout_add: out")
     _rng(rng, "dropout_add")
     x, residual, rng, out = _ptrs(x, residual, rng, out)
     _check(lib().dropout_add(x, residual, rows, cols, dt, p, rng, out, _stream(stream)),
@@ -693,10 +696,11 @@ def dropout_add_layer_norm(x: torch.Tensor, residual, p: float, rng, weight, bia
                            stream=None) -> None:
     """z = dropout_add(x, residual) and y = layer_norm(z) in one pass."""
     dt = _dtype(x, "dropout_add_layer_norm: x")
-    rows, cols = _last(x, "dropout_add_layer_norm: x")
-    _like(residual, x, "dropout_add_layer_norm: residual")
-    _like(z, x, "dropout_add_layer_norm: z")
-    _like(y, x, "dropout_add_layer_norm: y")
+    x_shape = x.shape
+    rows, cols = _last(x, x_shape, "dropout_add_layer_norm: x")
+    _like(residual, x.dtype, x_shape, "dropout_add_layer_norm: residual")
+    _like(z, x.dtype, x_shape, "dropout_add_layer_norm: z")
+    _like(y, x.dtype, x_shape, "dropout_add_layer_norm: y")
     wt = _params((weight, bias), x.dtype, cols, "dropout_add_layer_norm: weight, bias")
     _floats(mean, rows, "dropout_add_layer_norm: mean")
     _floats(rstd, rows, "dropout_add_layer_norm: rstd")
@@ -717,9 +721,10 @@ def quantize_int8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=
     """INT8 codes q (x's shape) and one float32 scale per row: x is about q * scale,
     scale = amax / 127.  Rows are tokens, or the output channels of a weight."""
     dt = _dtype(x, "quantize_int8: x")
-    rows, cols = _last(x, "quantize_int8: x")
+    x_shape = x.shape
+    rows, cols = _last(x, x_shape, "quantize_int8: x")
     _int8(q, "quantize_int8: q")
-    if q.shape != x.shape:
+    if q.shape != x_shape:
         raise Fp8dpError("quantize_int8: q must have x's shape")
     _floats(scale, rows, "quantize_int8: scale")
     x, q, scale = _ptrs(x, q, scale)
@@ -731,12 +736,13 @@ def layer_norm_quantize_int8(x: torch.Tensor, weight, bias, eps: float, q: torch
     """quantize_int8 of layer_norm(x) in one pass; with residual and z of layer_norm(z),
     z = x + residual."""
     dt = _dtype(x, "layer_norm_quantize_int8: x")
-    rows, cols = _last(x, "layer_norm_quantize_int8: x")
-    _like(residual, x, "layer_norm_quantize_int8: residual")
-    _like(z, x, "layer_norm_quantize_int8: z")
+    x_shape = x.shape
+    rows, cols = _last(x, x_shape, "layer_norm_quantize_int8: x")
+    _like(residual, x.dtype, x_shape, "layer_norm_quantize_int8: residual")
+    _like(z, x.dtype, x_shape, "layer_norm_quantize_int8: z")
     wt = _params((weight, bias), x.dtype, cols, "layer_norm_quantize_int8: weight, bias")
     _int8(q, "layer_norm_quantize_int8: q")
-    if q.shape != x.shape:
+    if q.shape != x_shape:
         raise Fp8dpError("layer_norm_quantize_int8: q must have x's shape")
     _floats(scale, rows, "layer_norm_quantize_int8: scale")
     x, residual, weight, bias, z, q, scale = _ptrs(x, residual, weight, bias, z, q, scale)
@@ -749,12 +755,12 @@ def _int8_operands(name: str, a: torch.Tensor, b: torch.Tensor, b_scale, y: torc
     """(M, N, K, y's type, bias' type) of a product a [..., K] x b [N, K] -> y [..., N]."""
     _int8(b, "weight")
     yt = _dtype(y, "y")
-    M, K = _last(a, name)
+    M, K = _last(a, a.shape, name)
     if b.dim() != 2 or y.dim() != a.dim():
         raise Fp8dpError(f"{name}: shape mismatch")
     N, k = b.shape
     if k != K or y.size(-1) != N or y.numel() != M * N or \
-            (a.dim() > 2 and y.shape[:-1] != a.shape[:-1]):
+            (y.dim() > 2 and y.shape[:-1] != a.shape[:-1]):
         raise Fp8dpError(f"{name}: shape mismatch")
     _floats(b_scale, N, "weight scale")
     return M, N, K, yt, yt if bias is None else _params((bias,), y.dtype, N, "bias")

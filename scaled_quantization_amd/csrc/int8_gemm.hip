@@ -161,7 +161,7 @@ static int launch_any(const char* what, const I8Args& g, void* workspace, int64_
                       hipStream_t stream) {
   const int64_t tiles = (((int64_t)g.M + 64 * TW - 1) / (64 * TW)) *
                         (((int64_t)g.N + 64 * TW - 1) / (64 * TW));
-  if (tiles > 0x7FFFFFFF) {
+  if (tiles * 256 > 0xFFFFFFFF) {   // threads of a launch
     set_error("%s: shape too large", what);
     return FP8DP_EINVAL;
   }

@@ -191,7 +191,7 @@ template <typename T, int WM, int WN, int TM, int TN, int S>
 static int launch_tile(const char* what, const I8Args& g, hipStream_t stream) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
   const int64_t tiles = (((int64_t)g.M + BM - 1) / BM) * (((int64_t)g.N + BN - 1) / BN);
-  if (tiles > 0x7FFFFFFF) {
+  if (tiles * 64 * WM * WN > 0xFFFFFFFF) {   // threads of a launch
     set_error("%s: shape too large", what);
     return FP8DP_EINVAL;
   }

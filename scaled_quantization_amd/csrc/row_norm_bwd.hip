@@ -294,41 +294,44 @@ __global__ __launch_bounds__(1024) void k_norm_parts(const float* parts, int npa
   typedef float pair_t __attribute__((ext_vector_type(2), aligned(4)));
   __shared__ float lds[64][33];
   const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
-  const int64_t width = 2 * (int64_t)cols;
-  const int64_t c = (int64_t)blockIdx.x * 32 + 2 * lane;
-  pair_t s = {0.0f, 0.0f};
-  if (c < width) {
-#pragma unroll 8
-    for (int i = group; i < nparts; i += 64)
-      s += *reinterpret_cast<const pair_t*>(parts + i * width + c);
-  }
-  lds[group][2 * lane] = s.x;
-  lds[group][2 * lane + 1] = s.y;
-  __syncthreads();
-  // 32 columns x 8 ranges of 8, then the 8
-  float v = 0.0f;
   const int col = threadIdx.x & 31, part = threadIdx.x >> 5;
-  if (part < 8) {
+  const int64_t width = 2 * (int64_t)cols;
+  for (int64_t c0 = (int64_t)blockIdx.x * 32; c0 < width; c0 += (int64_t)gridDim.x * 32) {
+    const int64_t c = c0 + 2 * lane;
+    pair_t s = {0.0f, 0.0f};
+    if (c < width) {
+#pragma unroll 8
+      for (int i = group; i < nparts; i += 64)
+        s += *reinterpret_cast<const pair_t*>(parts + i * width + c);
+    }
+    lds[group][2 * lane] = s.x;
+    lds[group][2 * lane + 1] = s.y;
+    __syncthreads();
+    // 32 columns x 8 ranges of 8, then the 8
+    float v = 0.0f;
+    if (part < 8) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v += lds[part * 8 + i][col];
-  }
-  __syncthreads();
-  if (part < 8) lds[part][col] = v;
-  __syncthreads();
-  const int64_t o = (int64_t)blockIdx.x * 32 + col;
-  if (part == 0 && o < width) {
-    float total = 0.0f;
+      for (int i = 0; i < 8; ++i) v += lds[part * 8 + i][col];
+    }
+    __syncthreads();
+    if (part < 8) lds[part][col] = v;
+    __syncthreads();
+    if (part == 0 && c0 + col < width) {
+      float total = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) total += lds[i][col];
-    if (o < cols) dweight[o] = total;
-    else dbias[o - cols] = total;
+      for (int i = 0; i < 8; ++i) total += lds[i][col];
+      if (c0 + col < cols) dweight[c0 + col] = total;
+      else dbias[c0 + col - cols] = total;
+    }
+    __syncthreads();
   }
 }
 
 static int launch_parts(const NormBwdArgs& a, int nparts, float* dweight, float* dbias,
                         hipStream_t stream) {
-  hipLaunchKernelGGL(k_norm_parts, dim3((unsigned)((2 * (int64_t)a.cols + 31) / 32)), dim3(1024), 0,
-                     stream, a.parts, nparts, a.cols, dweight, dbias);
+  const int64_t blocks = std::min<int64_t>((2 * (int64_t)a.cols + 31) / 32, 1 << 16);
+  hipLaunchKernelGGL(k_norm_parts, dim3((unsigned)blocks), dim3(1024), 0, stream, a.parts,
+                     nparts, a.cols, dweight, dbias);
   return check_launch("layer_norm_backward");
 }
 

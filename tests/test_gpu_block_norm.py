@@ -275,6 +275,30 @@ def test_dropout_add(t, cols):
                 assert np.array_equal((f64(out) != 0), (f != 0) & (f64(x) != 0))
 
 
+@pytest.mark.parametrize("rows, cols", [(1, 30_000_001), (30_000_001, 1), (70_001, 513), (3, 4_000_003)])
+def test_dropout_add_long_or_many_rows(rows, cols):
+    # more vectors than one pass of the grid takes, in one row, in rows of one element and between
+    x = draw((rows, cols), torch.bfloat16, 1)
+    out = torch.empty_like(x, device=DEV)
+    sq.dropout_add(x.to(DEV), None, 0.5, rng_words(), out)
+    f = OB.drop_factor(rows, cols, 0.5, SEED, OFFSET)
+    assert np.array_equal(f64(out), f64(x) * f)
+
+
+@pytest.mark.parametrize("cols", [300_001, 1_100_000])
+def test_layer_norm_backward_very_long_rows(cols):
+    t, rows = torch.bfloat16, 2
+    z, dy = draw((rows, cols), t, 1), draw((rows, cols), t, 2)
+    mean, rstd = z.float().mean(1), torch.ones(rows)
+    dz, dw, db = torch.empty_like(z, device=DEV), torch.empty(cols, device=DEV), torch.empty(cols, device=DEV)
+    sq.layer_norm_backward(dy.to(DEV), z.to(DEV), None, mean.to(DEV), rstd.to(DEV), dz, dw, db,
+                           torch.empty(2 * rows * cols, device=DEV))
+    d, h = f64(dy), f64(z) - f64(mean)[:, None]
+    # dweight sees mean's rounding (U of z and mean) and three roundings per row
+    close(dw, (d * h).sum(0), 8 * U * (np.abs(d) * (np.abs(h) + 1)).sum(0) + 1e-30, "dweight")
+    close(db, d.sum(0), 2 * U * np.abs(d).sum(0) + 1e-30, "dbias")
+
+
 def test_dropout_drops_what_is_not_finite_and_works_in_place():
     x = draw((4, 100), torch.bfloat16, 3)
     x[:, ::7] = float("inf")

@@ -121,7 +121,8 @@ def check_product(y, a, b, sa, sb, bias, t, what, rows=None):
     close(y, ref, 5 * U * mag + half(t) * np.abs(ref) + tiny(t), what)
 
 
-SHAPES = [(1, 1, 1), (1, 4096, 4096), (2, 17, 15), (3, 64, 16), (5, 130, 129), (16, 256, 128), (17, 250, 1000),
+SHAPES = [(1, 1, 1), (1, 4096, 4096), (2, 17, 15), (3, 64, 16), (5, 130, 129), (16, 256, 128), (17, 250, 1000), (5, 60, 1040), (40, 100, 400),
+          (33, 50, 272), (12, 33, 2064), (60, 17, 4240),
           (31, 1023, 777), (48, 512, 4096), (64, 64, 64), (65, 129, 257), (100, 300, 2000), (128, 128, 128),
           (129, 4, 4096), (200, 1000, 4112), (256, 256, 256), (257, 255, 1024), (300, 2049, 640),
           (512, 768, 1536), (777, 1023, 1001), (1000, 40, 32), (1024, 2304, 768), (2048, 512, 144),
@@ -219,7 +220,9 @@ def test_int8_gemm_rows_past_32_bits():
 
 
 # ------------------------------------------------------------------ linear layer
-@pytest.mark.parametrize("M, N, K", [(1, 4096, 4096), (1, 17, 5), (4, 1000, 3000), (8, 256, 8192), (16, 512, 1001),
+@pytest.mark.parametrize("M, N, K", [(1, 4096, 4096), (1, 17, 5), (2, 300, 4096), (3, 1000, 2048),
+                                     (4, 512, 4096), (4, 64, 16), (2, 33, 144), (1, 40, 16384), (1, 20, 65536),
+                                     (3, 17, 1040), (4, 1000, 3000), (8, 256, 8192), (16, 512, 1001),
                                      (17, 512, 512), (48, 4096, 4096), (129, 1000, 1000), (777, 1023, 1001),
                                      (1500, 1024, 2048)])
 @pytest.mark.parametrize("t", TYPES, ids=IDS)
@@ -246,7 +249,7 @@ def test_int8_linear(t, M, N, K):
 
 
 def test_int8_linear_row_that_is_not_finite():
-    for M in (1, 3, 40):
+    for M in (1, 2, 3, 4, 40):
         x = draw((M, 512), torch.bfloat16, 1)
         x[M - 1, 7] = float("nan")
         w8, w_scale = codes_of(draw((64, 512), torch.bfloat16, 2))

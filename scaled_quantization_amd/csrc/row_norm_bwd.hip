@@ -338,13 +338,17 @@ static int launch_parts(const NormBwdArgs& a, int nparts, float* dweight, float*
 template <typename T, int NV, int THR, bool DROP, bool STREAM>
 static int launch_bwd_as(const NormBwdArgs& a, float* dweight, float* dbias, hipStream_t stream) {
   constexpr int RPB = THR == 64 ? kBwdWaves : 1;
-  // as many workgroups as the device holds at once: all walk the same number of rows
+  // A compute unit gets waves for 16 vectors of a row and no more: each has two rows of loads in
+  // flight, and more of them only spread the reads and writes over more of memory (per
+  // compute unit 8 waves of 2 vectors against 12: 65536 x 4096 270 / 298 us, 262144 x 768
+  // 201 / 208, 16384 x 768 20.0 / 21.7; 16 waves of 1 against 8: 30001 x 1600 60 / 68).  All are
+  // resident at once and walk the same number of rows.
   static const int resident = [] {
     int n = 0;
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, (k_norm_bwd<T, NV, THR, DROP, STREAM>), RPB * THR,
-                                                     0) != hipSuccess || n < 1)
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, (k_norm_bwd<T, NV, THR, DROP, STREAM>),
+                                                     RPB * THR, 0) != hipSuccess || n < 1)
       n = 1;
-    return n;
+    return std::min(n, std::max(1, 16 * 64 / (NV * RPB * THR)));
   }();
   const int64_t cap = std::min<int64_t>(FP8DP_NORM_PARTS, (int64_t)num_cus() * resident);
   const int64_t grid = std::min<int64_t>((a.rows + RPB - 1) / RPB, cap);

@@ -75,7 +75,7 @@ __device__ __forceinline__ void store_out4(const I8Args& g, int64_t m, int n, fl
                                            const float sb[4], const float bias[4], const v4i_t& c) {
   float v[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = (float)c[j] * sa * sb[j] + bias[j];
+  for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf((float)c[j] * sa, sb[j], bias[j]);
   T* const p = static_cast<T*>(g.y) + m * g.N + n;
   if (n + 4 <= g.N) {
     if constexpr (sizeof(T) == 4) {
@@ -129,56 +129,76 @@ __device__ __forceinline__ void widen_bias4(const I8Args& g, const RawCols4& r, 
   }
 }
 
-// Epilogue of a wave's TM x TN tiles of 32 x 32 at rows m0, columns n0.  In such a tile the lane
-// holds token lane % 32 and register r channel 8 (r / 4) + 4 (lane / 32) + r % 4: stored
-// from there, a row gets 8 bytes at a time.  The wave turns its tiles in its own 32 x 32 TN words
-// of LDS, 32 tokens at a time as binary32 (sum times token scale), and reads them back
-// with 8 consecutive channels per lane, whose scales and bias it then holds for all rows,
-// and whole cache lines per row to store.  16-byte chunks are swizzled by row against
-// bank conflicts.
+// What the outputs of a tile of BM tokens x BN channels need beside its sums, in LDS: loaded
+// while the first stages travel, so that the epilogue waits for nothing from memory.
+template <int BM, int BN>
+struct TileScales {
+  float sa[BM], sb[BN], bias[BN];
+};
+template <typename T, int BM, int BN>
+__device__ __forceinline__ void load_scales(const I8Args& g, TileScales<BM, BN>& s, int m0, int n0,
+                                            int tid, int threads) {
+  for (int i = tid; i < BM; i += threads) s.sa[i] = g.sa[m0 + i < g.M ? m0 + i : g.M - 1];
+  for (int i = tid; i < BN; i += threads) {
+    const int n = n0 + i < g.N ? n0 + i : g.N - 1;
+    s.sb[i] = g.sb[n];
+    s.bias[i] = g.bias == nullptr ? 0.0f
+                : sizeof(T) == 4 || g.bias_f32 ? static_cast<const float*>(g.bias)[n]
+                                               : to_f32(static_cast<const T*>(g.bias)[n]);
+  }
+}
+
+// Epilogue of a wave's TM x TN tiles of 32 x 32 at row wr, column wc of a tile at m0, n0.  In such a
+// tile the lane holds token lane % 32 and register r channel 8 (r / 4) + 4 (lane / 32) + r % 4:
+// stored from there, a row gets 8 bytes at a time.  The wave turns its tiles in its own
+// 32 x 32 TN words of LDS, 32 tokens at a time as binary32 (sum times token scale), and reads them
+// back with 8 consecutive channels per lane, whose scales and bias it then holds for
+// all rows, and whole cache lines per row to store.  16-byte chunks are swizzled by row
+// against bank conflicts.
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
-template <typename T, int TM, int TN>
+template <typename T, int TM, int TN, int BM, int BN>
 __device__ __forceinline__ void turn_out(const I8Args& g, const v16i_t (&acc)[TM][TN],
-                                         uint8_t* part, int m0, int n0, int lane) {
+                                         uint8_t* part, const TileScales<BM, BN>& scales, int m0,
+                                         int n0, int wr, int wc, int lane) {
   constexpr int CW = TN * 32, LPR = CW / 8, RPI = 64 / LPR;   // columns, lanes per row, rows per step
   const int frow = lane & 31, fhalf = lane >> 5;
   auto at = [&](int r, int c) {   // byte of chunk c (4 channels) of row r
     return r * CW * 4 + ((c ^ (TN == 1 ? (r >> 1) & 7 : r & 15)) << 4);
   };
-  const int n = n0 + (lane % LPR) * 8;
-  const RawCols4 c0 = load_cols4<T>(g, n), c1 = load_cols4<T>(g, n + 4);
-  float sa[TM];
+  const int col = wc + (lane % LPR) * 8, n = n0 + col, row = wr + lane / LPR;
+  float sb[8], bias[8];
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int m = m0 + 32 * i + frow;
-    sa[i] = g.sa[m < g.M ? m : g.M - 1];
+  for (int k = 0; k < 8; ++k) {
+    sb[k] = scales.sb[col + k];
+    bias[k] = scales.bias[col + k];
   }
-  float bias[8];
-  widen_bias4<T>(g, c0, bias);
-  widen_bias4<T>(g, c1, bias + 4);
+  T* out = static_cast<T*>(g.y) + (int64_t)(m0 + row) * g.N + n;
+  const int left = n < g.N ? g.M - m0 - row : 0, wide = g.N - n;   // rows and columns to the edge
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
+    const float sa = scales.sa[wr + 32 * i + frow];
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         f32x4_t v;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = (float)acc[i][j][4 * q + r] * sa[i];
+        for (int r = 0; r < 4; ++r) v[r] = (float)acc[i][j][4 * q + r] * sa;
         *reinterpret_cast<f32x4_t*>(part + at(frow, j * 8 + 2 * q + fhalf)) = v;
       }
 #pragma unroll
     for (int s = 0; s < 32 / RPI; ++s) {
-      const int r = s * RPI + lane / LPR, m = m0 + 32 * i + r, c = (lane % LPR) * 2;
+      const int r = s * RPI + lane / LPR, c = (lane % LPR) * 2;
       const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(part + at(r, c));
       const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(part + at(r, c + 1));
       float v[8];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        v[k] = lo[k] * c0.sb[k] + bias[k];
-        v[k + 4] = hi[k] * c1.sb[k] + bias[k + 4];
+        v[k] = __builtin_fmaf(lo[k], sb[k], bias[k]);
+        v[k + 4] = __builtin_fmaf(hi[k], sb[k + 4], bias[k + 4]);
       }
-      if (m < g.M && n < g.N) store8(static_cast<T*>(g.y) + (int64_t)m * g.N + n, g.N - n, v);
+      if (32 * i + s * RPI < left) store8(out, wide, v);
+      out += (int64_t)RPI * g.N;
     }
   }
 }

@@ -35,6 +35,7 @@ template <typename T, int TW, int PF, bool TINY>
 __global__ __launch_bounds__(256) void k_i8_any(I8Args g, v4i_t* partial) {
   constexpr int R = 64 * TW, TILE = R * kBK, L = R / 32;   // rows, bytes of a tile, chunks per thread
   __shared__ __attribute__((aligned(16))) uint8_t lds[4 * TILE];
+  __shared__ TileScales<R, R> scales;
   const int tiles_n = (g.N + R - 1) / R;
   const int ntiles = ((g.M + R - 1) / R) * tiles_n;
   const int tile = tile_of_block(blockIdx.x, ntiles);
@@ -94,6 +95,7 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args g, v4i_t* partial) {
   // PF later
 #pragma unroll
   for (int u = 0; u < PF; ++u) load(u, first + u);
+  if (gridDim.y == 1) load_scales<T>(g, scales, m0, n0, tid, 256);
   put(0, 0, 0);
   load(0, first + PF);
   __syncthreads();
@@ -130,7 +132,7 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args g, v4i_t* partial) {
     }
     return;
   }
-  turn_out<T, TW, TW>(g, acc, lds + wave * 32 * TW * 128, m0 + wm, n0 + wn, lane);
+  turn_out<T>(g, acc, lds + wave * 32 * TW * 128, scales, m0, n0, wm, wn, lane);
 }
 
 // Joins the ranges' sums of a tile and writes its outputs.
@@ -138,9 +140,11 @@ template <typename T, int TW>
 __global__ __launch_bounds__(256) void k_i8_join(I8Args g, const v4i_t* partial, int ranges) {
   constexpr int R = 64 * TW;
   __shared__ __attribute__((aligned(16))) uint8_t lds[4 * 32 * TW * 128];
+  __shared__ TileScales<R, R> scales;
   const int tiles_n = (g.N + R - 1) / R, tile = blockIdx.x;
   const int m0 = (tile / tiles_n) * R, n0 = (tile % tiles_n) * R;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  load_scales<T>(g, scales, m0, n0, tid, 256);
   v16i_t acc[TW][TW];
 #pragma unroll
   for (int i = 0; i < TW * TW * 4; ++i) {
@@ -152,8 +156,9 @@ __global__ __launch_bounds__(256) void k_i8_join(I8Args g, const v4i_t* partial,
 #pragma unroll
     for (int r = 0; r < 4; ++r) c[4 * (i % 4) + r] = sum[r];
   }
-  turn_out<T, TW, TW>(g, acc, lds + wave * 32 * TW * 128, m0 + (wave >> 1) * 32 * TW,
-                      n0 + (wave & 1) * 32 * TW, lane);
+  __syncthreads();
+  turn_out<T>(g, acc, lds + wave * 32 * TW * 128, scales, m0, n0, (wave >> 1) * 32 * TW,
+              (wave & 1) * 32 * TW, lane);
 }
 
 template <typename T, int TW, int PF, bool TINY = false>

@@ -38,7 +38,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_i8_tile(I8Args g) {
   constexpr int ASZ = BM * kBK, SLOT = (BM + BN) * kBK;
   static_assert(W % 2 == 0, "the swizzle of a copy");
   constexpr int LA = BM / 8 / W, LB = BN / 8 / W, NCOPY = LA + LB;   // copies of a wave per stage
-  __shared__ __attribute__((aligned(16))) uint8_t lds[S * SLOT];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[S * SLOT + sizeof(TileScales<BM, BN>)];
+  TileScales<BM, BN>& scales = *reinterpret_cast<TileScales<BM, BN>*>(lds + S * SLOT);
 
   const int tiles_n = (g.N + BN - 1) / BN;
   const int ntiles = ((g.M + BM - 1) / BM) * tiles_n;
@@ -140,6 +141,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_i8_tile(I8Args g) {
 #pragma unroll
   for (int s = 0; s < S; ++s)
     if (s < KT) issue(s);
+  load_scales<T>(g, scales, m0, n0, threadIdx.x, 64 * W);
   if (KT >= S) wait_vmcnt<(S - 1) * NCOPY>();
   else wait_vmcnt<0>();
   stage_barrier();
@@ -184,7 +186,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_i8_tile(I8Args g) {
   stage(kt, no{}, no{});
 
   static_assert(W * 32 * TN * 128 <= S * SLOT, "the waves' parts fit the ring");
-  turn_out<T, TM, TN>(g, acc, lds + wave * 32 * TN * 128, m0 + wr, n0 + wc, lane);
+  turn_out<T>(g, acc, lds + wave * 32 * TN * 128, scales, m0, n0, wr, wc, lane);
 }
 
 template <typename T, int WM, int WN, int TM, int TN, int S>

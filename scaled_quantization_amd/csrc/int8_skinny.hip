@@ -104,7 +104,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_i8_few(I8Args g, const T* x) {
     // the tokens' chunks, one copy of 64 per wave in turn
     const int chunks = M * K * (int)sizeof(T) / 16, steps = (chunks + 64 * WAVES - 1) / (64 * WAVES);
     float* const scale = reinterpret_cast<float*>(tokens + steps * 1024 * WAVES);
-    uint32_t* const top = reinterpret_cast<uint32_t*>(scale + 8);
+    uint32_t* const top = reinterpret_cast<uint32_t*>(scale + 16);
     for (int s = 0; s < steps; ++s) {
       const int q = (s * WAVES + wave) * 64 + lane;
       copy16_to_lds(reinterpret_cast<const uint8_t*>(x) + (size_t)(q < chunks ? q : chunks - 1) * 16,
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_i8_few(I8Args g, const T* x) {
     });
     stage_barrier();
     // a wave takes one of `parts` ranges of a token's vectors at a time
-    const int parts = M == 1 ? WAVES : M == 2 ? WAVES / 2 : WAVES / 4, items = M * parts;
+    const int parts = M == 1 ? WAVES : M == 2 ? WAVES / 2 : M <= 4 ? WAVES / 4 : 1, items = M * parts;
     const int nvec = K / 8, per = (nvec + parts - 1) / parts;
     auto vector = [&](int i, int v, float* w) {
       const T* const p = reinterpret_cast<const T*>(tokens) + (i / parts) * K + v * 8;
@@ -285,7 +285,7 @@ static int launch_few_any(const char* what, const I8Args& g, hipStream_t stream)
 
 template <typename T>
 static int skinny_type(const char* what, const I8Args& g, const void* x, hipStream_t stream) {
-  if (x != nullptr) return launch_few<T, 1, 8, 4, true>(what, g, x, stream);
+  if (x != nullptr) return launch_few<T, 2, 8, 4, true>(what, g, x, stream);
   if (!rows16(g)) {
     if (g.M <= 16) return launch_few_any<T, 1>(what, g, stream);
     if (g.M <= 32) return launch_few_any<T, 2>(what, g, stream);

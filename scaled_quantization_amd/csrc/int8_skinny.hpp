@@ -10,12 +10,12 @@ constexpr int kFewTokens = 64;
 // plus 16 so that the rows of a fragment read start 16 bytes apart in the banks.
 __host__ __device__ constexpr int skinny_stride(int K) { return (K + 127) / 128 * 128 + 16; }
 
-// LDS of the casting form beside its ring: codes, tokens (in copies of 1 KB), scales and the
-// parts' largest magnitudes.
+// LDS of the casting form beside its ring: codes, tokens (in copies of 1 KB), 16 scales and the
+// largest magnitudes of up to 4 waves parts.
 inline size_t skinny_cast_bytes(int M, int K, int size, int waves) {
   const int64_t chunks = (int64_t)M * K * size / 16, group = 64 * waves;
   return (size_t)M * skinny_stride(K) + (size_t)((chunks + group - 1) / group) * group * 16 +
-         4 * (8 + 4 * waves);
+         4 * (16 + 4 * waves);
 }
 
 // x: tokens of the output's type to cast in the kernel (int8_linear), or NULL: codes in g.a.
@@ -23,13 +23,15 @@ inline size_t skinny_cast_bytes(int M, int K, int size, int waves) {
 int skinny_i8(const char* what, fp8dp_dtype yt, const I8Args& g, const void* x,
               hipStream_t stream);
 
-// Whether the casting form takes the tokens at x: up to 4, rows of whole chunks, and at most 64 KB of
-// LDS beside the ring of 64 KB.  Every workgroup casts all of them.  Measured with 4096 x 4096 weights:
-// 5.9 us for 1 token, 6.3 for 2, 6.8 for 4, against 5.7 to 5.8 for the product alone and about 4 for
-// a launch that casts.
+// Whether the casting form takes the tokens at x: up to 16 of 16384 values together, or one; rows of
+// whole chunks; at most 64 KB of LDS beside the ring of 64 KB.  Every workgroup casts all of them,
+// which against a launch of its own (in a graph, where a launch costs least) gains at
+// few values and breaks even at 16384: 1 x 4096 x 4096 5.0 us for 6.6, 4 x 4096 x 4096 6.2 for 6.8,
+// 8 x 1024 x 1024 4.2 for 5.3, 16 x 4096 x 1024 5.6 for 5.4.
 inline bool skinny_casts(const I8Args& g, const void* x, int size) {
-  return g.M <= 4 && g.K % 16 == 0 && g.ldb % 16 == 0 && aligned16(x) && aligned16(g.b) &&
-         (int64_t)g.M * g.K <= 65536 && skinny_cast_bytes(g.M, g.K, size, 8) <= 64 * 1024;
+  return g.M <= 16 && (g.M == 1 || (int64_t)g.M * g.K <= 16384) && g.K <= 65536 &&
+         g.K % 16 == 0 && g.ldb % 16 == 0 && aligned16(x) && aligned16(g.b) &&
+         skinny_cast_bytes(g.M, g.K, size, 8) <= 64 * 1024;
 }
 
 }  // namespace fp8dp

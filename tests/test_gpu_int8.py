@@ -222,7 +222,8 @@ def test_int8_gemm_rows_past_32_bits():
 # ------------------------------------------------------------------ linear layer
 @pytest.mark.parametrize("M, N, K", [(1, 4096, 4096), (1, 17, 5), (2, 300, 4096), (3, 1000, 2048),
                                      (4, 512, 4096), (4, 64, 16), (2, 33, 144), (1, 40, 16384), (1, 20, 65536),
-                                     (3, 17, 1040), (4, 1000, 3000), (8, 256, 8192), (16, 512, 1001),
+                                     (3, 17, 1040), (4, 1000, 3000), (5, 50, 1024), (8, 300, 2048),
+                                     (9, 40, 400), (16, 128, 1024), (13, 70, 272), (8, 256, 8192), (16, 512, 1001),
                                      (17, 512, 512), (48, 4096, 4096), (129, 1000, 1000), (777, 1023, 1001),
                                      (1500, 1024, 2048)])
 @pytest.mark.parametrize("t", TYPES, ids=IDS)
@@ -249,7 +250,7 @@ def test_int8_linear(t, M, N, K):
 
 
 def test_int8_linear_row_that_is_not_finite():
-    for M in (1, 2, 3, 4, 40):
+    for M in (1, 2, 3, 4, 7, 16, 40):
         x = draw((M, 512), torch.bfloat16, 1)
         x[M - 1, 7] = float("nan")
         w8, w_scale = codes_of(draw((64, 512), torch.bfloat16, 2))

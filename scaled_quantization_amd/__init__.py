@@ -561,19 +561,17 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _F32, _I8 = torch.float32, torch.int8
 
 
-def _device() -> int:
-    """The current device; -2, which no tensor is on, where there is none."""
+def _args(stream, *ts) -> list:
+    """_p of each tensor, with the checks that pass kept cheap, and the stream's handle."""
     try:
-        return _current_device()
+        device = _current_device()
     except RuntimeError:
-        return -2
-
-
-def _ptrs(*ts) -> list:
-    """_p of each tensor, with the checks that pass kept cheap."""
-    device = _device()
-    return [None if t is None else
-            t.data_ptr() if t.get_device() == device and t.is_contiguous() else _p(t) for t in ts]
+        device = -2                    # there is no device, and no tensor is on it
+    out = [None if t is None else
+           t.data_ptr() if t.get_device() == device and t.is_contiguous() else _p(t) for t in ts]
+    out.append(_raw_stream(device) if stream is None and _raw_stream is not None
+               else _stream(stream))
+    return out
 
 
 def _dtype(t: torch.Tensor, what: str) -> int:
@@ -639,9 +637,9 @@ def layer_norm(x: torch.Tensor, weight, bias, eps: float, y: torch.Tensor, mean=
     wt = _params((weight, bias), x.dtype, cols, "layer_norm: weight, bias")
     _floats(mean, rows, "layer_norm: mean")
     _floats(rstd, rows, "layer_norm: rstd")
-    x, weight, bias, y, mean, rstd = _ptrs(x, weight, bias, y, mean, rstd)
-    _check(lib().layer_norm(x, weight, bias, rows, cols, dt, wt, eps, y, mean, rstd,
-                            _stream(stream)), "layer_norm")
+    x, weight, bias, y, mean, rstd, s = _args(stream, x, weight, bias, y, mean, rstd)
+    _check(lib().layer_norm(x, weight, bias, rows, cols, dt, wt, eps, y, mean, rstd, s),
+           "layer_norm")
 
 
 def layer_norm_backward(dy: torch.Tensor, z: torch.Tensor, weight, mean: torch.Tensor,
@@ -670,11 +668,10 @@ def layer_norm_backward(dy: torch.Tensor, z: torch.Tensor, weight, mean: torch.T
             or workspace.numel() < 2 * min(rows, NORM_PARTS) * cols):
         raise Fp8dpError("layer_norm_backward: workspace needs 2 * min(rows, "
                          f"{NORM_PARTS}) * cols = {2 * min(rows, NORM_PARTS) * cols} float32")
-    (dy, z, weight, mean, rstd, dz_add, rng, dz, dx, dweight, dbias, workspace) = _ptrs(
-        dy, z, weight, mean, rstd, dz_add, rng, dz, dx, dweight, dbias, workspace)
+    (dy, z, weight, mean, rstd, dz_add, rng, dz, dx, dweight, dbias, workspace, s) = _args(
+        stream, dy, z, weight, mean, rstd, dz_add, rng, dz, dx, dweight, dbias, workspace)
     _check(lib().layer_norm_backward(dy, z, weight, mean, rstd, dz_add, rows, cols, dt, wt, p, rng,
-                                     dz, dx, dweight, dbias, workspace, _stream(stream)),
-           "layer_norm_backward")
+                                     dz, dx, dweight, dbias, workspace, s), "layer_norm_backward")
 
 
 def dropout_add(x: torch.Tensor, residual, p: float, rng, out: torch.Tensor, stream=None) -> None:
@@ -686,9 +683,8 @@ def dropout_add(x: torch.Tensor, residual, p: float, rng, out: torch.Tensor, str
     _like(residual, x.dtype, x_shape, "dropout_add: residual")
     _like(out, x.dtype, x_shape, "dropout_add: out")
     _rng(rng, "dropout_add")
-    x, residual, rng, out = _ptrs(x, residual, rng, out)
-    _check(lib().dropout_add(x, residual, rows, cols, dt, p, rng, out, _stream(stream)),
-           "dropout_add")
+    x, residual, rng, out, s = _args(stream, x, residual, rng, out)
+    _check(lib().dropout_add(x, residual, rows, cols, dt, p, rng, out, s), "dropout_add")
 
 
 def dropout_add_layer_norm(x: torch.Tensor, residual, p: float, rng, weight, bias, eps: float,
@@ -705,11 +701,10 @@ def dropout_add_layer_norm(x: torch.Tensor, residual, p: float, rng, weight, bia
     _floats(mean, rows, "dropout_add_layer_norm: mean")
     _floats(rstd, rows, "dropout_add_layer_norm: rstd")
     _rng(rng, "dropout_add_layer_norm")
-    x, residual, weight, bias, rng, z, y, mean, rstd = _ptrs(x, residual, weight, bias, rng, z, y,
-                                                             mean, rstd)
+    x, residual, weight, bias, rng, z, y, mean, rstd, s = _args(
+        stream, x, residual, weight, bias, rng, z, y, mean, rstd)
     _check(lib().dropout_add_layer_norm(x, residual, weight, bias, rows, cols, dt, wt, p, rng, eps,
-                                        z, y, mean, rstd, _stream(stream)),
-           "dropout_add_layer_norm")
+                                        z, y, mean, rstd, s), "dropout_add_layer_norm")
 
 
 def _int8(t: torch.Tensor, what: str) -> None:
@@ -727,8 +722,8 @@ def quantize_int8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=
     if q.shape != x_shape:
         raise Fp8dpError("quantize_int8: q must have x's shape")
     _floats(scale, rows, "quantize_int8: scale")
-    x, q, scale = _ptrs(x, q, scale)
-    _check(lib().quantize_int8(x, rows, cols, dt, q, scale, _stream(stream)), "quantize_int8")
+    x, q, scale, s = _args(stream, x, q, scale)
+    _check(lib().quantize_int8(x, rows, cols, dt, q, scale, s), "quantize_int8")
 
 
 def layer_norm_quantize_int8(x: torch.Tensor, weight, bias, eps: float, q: torch.Tensor,
@@ -745,9 +740,10 @@ def layer_norm_quantize_int8(x: torch.Tensor, weight, bias, eps: float, q: torch
     if q.shape != x_shape:
         raise Fp8dpError("layer_norm_quantize_int8: q must have x's shape")
     _floats(scale, rows, "layer_norm_quantize_int8: scale")
-    x, residual, weight, bias, z, q, scale = _ptrs(x, residual, weight, bias, z, q, scale)
+    x, residual, weight, bias, z, q, scale, s = _args(
+        stream, x, residual, weight, bias, z, q, scale)
     _check(lib().layer_norm_quantize_int8(x, residual, weight, bias, rows, cols, dt, wt, eps, z, q,
-                                          scale, _stream(stream)), "layer_norm_quantize_int8")
+                                          scale, s), "layer_norm_quantize_int8")
 
 
 def _int8_operands(name: str, a: torch.Tensor, b: torch.Tensor, b_scale, y: torch.Tensor,
@@ -776,9 +772,10 @@ def int8_gemm(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: 
     M, N, K, yt, bt = _int8_operands("int8_gemm", a, b, b_scale, y, bias)
     _floats(a_scale, M, "int8_gemm: a_scale")
     room = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    a, b, a_scale, b_scale, bias, y, workspace = _ptrs(a, b, a_scale, b_scale, bias, y, workspace)
-    _check(lib().int8_gemm(a, b, M, N, K, a_scale, b_scale, bias, yt, bt, y, workspace, room,
-                           _stream(stream)), "int8_gemm")
+    a, b, a_scale, b_scale, bias, y, workspace, s = _args(
+        stream, a, b, a_scale, b_scale, bias, y, workspace)
+    _check(lib().int8_gemm(a, b, M, N, K, a_scale, b_scale, bias, yt, bt, y, workspace, room, s),
+           "int8_gemm")
 
 
 def int8_linear_workspace(M: int, K: int) -> int:
@@ -795,9 +792,9 @@ def int8_linear(x: torch.Tensor, w8: torch.Tensor, w_scale: torch.Tensor, y: tor
         raise Fp8dpError(f"int8_linear: y must be of x's type, {x.dtype}, got {y.dtype}")
     M, N, K, yt, bt = _int8_operands("int8_linear", x, w8, w_scale, y, bias)
     room = workspace.numel() * workspace.element_size()
-    x, w8, w_scale, bias, y, workspace = _ptrs(x, w8, w_scale, bias, y, workspace)
-    _check(lib().int8_linear(x, w8, w_scale, bias, M, N, K, yt, bt, y, workspace, room,
-                             _stream(stream)), "int8_linear")
+    x, w8, w_scale, bias, y, workspace, s = _args(stream, x, w8, w_scale, bias, y, workspace)
+    _check(lib().int8_linear(x, w8, w_scale, bias, M, N, K, yt, bt, y, workspace, room, s),
+           "int8_linear")
 
 
 def fp8dp_bench_act_bf16(h: torch.Tensor, act: int, out: torch.Tensor, stream=None) -> None:

@@ -103,8 +103,8 @@ __device__ __forceinline__ Raw8<float> round8(const float v[8], float) {
   return r;
 }
 // Outputs are stored non-temporally: this kernel does not read them again, and they
-// displace fewer of the inputs from L2 (layer norm 16384 x 768 10.5 -> 10.1 us, with
-// dropout and residual 22.0 -> 18.5, 65536 x 4096 212 -> 205).  Loads are left alone:
+// displace fewer of the inputs from L2 (layer norm 16384 x 768 11.3 -> 10.4 us, with
+// dropout and residual 22.0 -> 19.0, layer norm 65536 x 4096 186 -> 179).  Loads are left alone:
 // inputs often come out of the cache that an earlier kernel filled (non-temporal loads at
 // 16384 x 768: 14.4 us).
 template <typename T>

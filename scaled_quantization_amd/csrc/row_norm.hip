@@ -339,9 +339,9 @@ __global__ __launch_bounds__(THR == 64 ? 256 : THR) void k_row_loop(RowArgs a) {
 // moved in all: the last-level cache has 256 MB) do best with few waves that walk many rows,
 // which spares them the parameters and masks; streams from memory with many
 // short ones, whose reads and writes the scheduler keeps apart.  Measured, 16 against
-// 256 waves: layer norm 16384 x 768 10.1 / 13.3 us, dropout + residual + norm 30001 x 1600 75 / 95;
-// layer norm 65536 x 4096 205 / 177, with dropout and residual 443 / 385.  The norm
-// with the cast is bound by its instructions either way (65536 x 4096: 168 / 178).
+// 256 waves: layer norm 16384 x 768 10.4 / 13.9 us, dropout + residual + norm 30001 x 1600 74 / 95;
+// layer norm 65536 x 4096 206 / 179, with dropout and residual 444 / 382.  The norm
+// with the cast is bound by its instructions either way (65536 x 4096: 167 / 180).
 constexpr int64_t kRowStreamBytes = (int64_t)512 << 20;
 
 template <typename T, int NV, int THR, bool DROP, bool NORM, bool QUANT>

@@ -360,7 +360,8 @@ static int launch_bwd_as(const NormBwdArgs& a, float* dweight, float* dbias, hip
 }
 
 // Beyond the 256 MB of the last-level cache: read past the caches (measured, with and without:
-// 65536 x 4096 300 / 312 us, 262144 x 768 211 / 219; 16384 x 768, which they hold, 23.6 / 21.0).
+// 65536 x 4096 271 / 290 us, 262144 x 768 198 / 213; 16384 x 768, which they hold, 21.1 / 20.4
+// and with dropout and residual 31.0 / 28.2).
 template <typename T, int NV, int THR, bool DROP>
 static int launch_bwd(const NormBwdArgs& a, float* dweight, float* dbias, hipStream_t stream) {
   const int64_t tensors = 3 + (a.dz_add != nullptr) + (a.dx != nullptr);

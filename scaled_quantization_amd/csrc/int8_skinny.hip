@@ -145,17 +145,20 @@ __global__ __launch_bounds__(64 * WAVES) void k_i8_few(I8Args g, const T* x) {
       const RowScale s = row_scale(plain ? m : 0x3F800000u);
       if (p == 0 && lane == 0)
         scale[r] = plain ? __uint_as_float(m) / 127.0f : m == 0 ? 0.0f : __builtin_nanf("");
-      // the last range also clears the codes up to the end of the LDS row
-      const int v1 = p == parts - 1 ? stride / 8 : (p + 1) * per < nvec ? (p + 1) * per : nvec;
+      const int v1 = (p + 1) * per < nvec ? (p + 1) * per : nvec;
       for (int v = p * per + lane; v < v1; v += 64) {
         uint2 code = {0u, 0u};
-        if (plain && v < nvec) {
+        if (plain) {
           float w[8];
           vector(i, v, w);
           code = codes8<sizeof(T) == 4>(w, s);
         }
         *reinterpret_cast<uint2*>(codes + r * stride + v * 8) = code;
       }
+      // the wave of the first range also clears the codes from K to the end of the LDS row (16 vectors
+      // at most); the others may be empty, with nvec anywhere among their starts
+      if (p == 0 && nvec + lane < stride / 8)
+        *reinterpret_cast<uint2*>(codes + r * stride + (nvec + lane) * 8) = uint2{0u, 0u};
     }
     __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     stage_barrier();

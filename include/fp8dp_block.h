@@ -121,8 +121,8 @@ int layer_norm_quantize_int8(const void* x, const void* residual, const void* we
    are few tiles of y (16 MiB is all that takes), and copy operands whose rows do not start
    at multiples of 16 bytes into rows that do (K rounded up to 16 bytes a row of each); NULL
    or any size is fine.  Calls that share a workspace must not overlap in time.
-   Errors: EINVAL for a NULL operand, scale or y, M or N outside 1 .. 2^30, K
-   outside 1 .. FP8DP_INT8_MAX_K, unknown types, a misaligned pointer
+   Errors: EINVAL for a NULL operand, scale or y, M or N outside 1 .. 2^30, M * N
+   above 2^40, K outside 1 .. FP8DP_INT8_MAX_K, unknown types, a misaligned pointer
    (workspace: 16 bytes), or workspace_bytes < 0. */
 int int8_gemm(const int8_t* a, const int8_t* b, int64_t M, int64_t N, int64_t K,
               const float* a_scale, const float* b_scale, const void* bias, fp8dp_dtype yt,
@@ -135,7 +135,7 @@ int64_t int8_linear_workspace(int64_t M, int64_t K);
 
 /* quantize_int8 of x [M x K] (type dt) and int8_gemm with w8 [N x K] and w_scale
    [N]; y and bias as there, y of type dt.  workspace: 16-byte aligned, at least
-   int8_linear_workspace(M, K) bytes. */
+   int8_linear_workspace(M, K) bytes.  Errors: as int8_gemm's. */
 int int8_linear(const void* x, const int8_t* w8, const float* w_scale, const void* bias, int64_t M,
                 int64_t N, int64_t K, fp8dp_dtype dt, fp8dp_dtype bt, void* y, void* workspace,
                 int64_t workspace_bytes, hipStream_t stream);

@@ -21,11 +21,24 @@ struct I8Args {
   const void* bias;
   bool bias_f32;
   void* y;
+  int first = 0;                // tile (or group of channels) of workgroup 0: for_blocks()
 };
 
 // Whether the rows of both operands start at multiples of 16 bytes and K is one too.
 inline bool rows16(const I8Args& g) {
   return g.K % 16 == 0 && g.lda % 16 == 0 && g.ldb % 16 == 0 && aligned16(g.a) && aligned16(g.b);
+}
+
+// A launch has at most 2^32 - 1 threads, which workgroups of 512 reach at 2^23: more of them
+// go in several launches, each with the index of its first one.  launch(first, count).
+template <typename F>
+inline int for_blocks(int64_t blocks, F&& launch) {
+  constexpr int64_t kMost = (int64_t)1 << 22;   // (a multiple of 8: the XCDs' turns go on)
+  for (int64_t first = 0; first < blocks; first += kMost) {
+    const int rc = launch((int)first, (unsigned)std::min(blocks - first, kMost));
+    if (rc) return rc;
+  }
+  return FP8DP_OK;
 }
 
 // What chunks past K are copied from.

@@ -38,7 +38,7 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args g, v4i_t* partial) {
   __shared__ TileScales<R, R> scales;
   const int tiles_n = (g.N + R - 1) / R;
   const int ntiles = ((g.M + R - 1) / R) * tiles_n;
-  const int tile = tile_of_block(blockIdx.x, ntiles);
+  const int tile = tile_of_block(g.first + (int)blockIdx.x, ntiles);
   const int m0 = (tile / tiles_n) * R, n0 = (tile % tiles_n) * R;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -166,10 +166,6 @@ static int launch_any(const char* what, const I8Args& g, void* workspace, int64_
                       hipStream_t stream) {
   const int64_t tiles = (((int64_t)g.M + 64 * TW - 1) / (64 * TW)) *
                         (((int64_t)g.N + 64 * TW - 1) / (64 * TW));
-  if (tiles * 256 > 0xFFFFFFFF) {   // threads of a launch
-    set_error("%s: shape too large", what);
-    return FP8DP_EINVAL;
-  }
   // K in ranges of at least 4 stages, as long as there are compute units without a tile
   int64_t ranges = 1;
   if (TW == 1 && !TINY) {
@@ -181,9 +177,13 @@ static int launch_any(const char* what, const I8Args& g, void* workspace, int64_
     if (stages < 32 || ranges < 2) ranges = 1;
   }
   v4i_t* const partial = static_cast<v4i_t*>(workspace);
-  hipLaunchKernelGGL((k_i8_any<T, TW, PF, TINY>), dim3((unsigned)tiles, (unsigned)ranges),
-                     dim3(256), 0, stream, g, partial);
-  const int rc = check_launch(what);
+  const int rc = for_blocks(tiles, [&](int first, unsigned count) {
+    I8Args part = g;
+    part.first = first;
+    hipLaunchKernelGGL((k_i8_any<T, TW, PF, TINY>), dim3(count, (unsigned)ranges), dim3(256), 0, stream,
+                       part, partial);
+    return check_launch(what);
+  });
   if (rc || ranges == 1) return rc;
   hipLaunchKernelGGL((k_i8_join<T, TW>), dim3((unsigned)tiles), dim3(256), 0, stream, g, partial,
                      (int)ranges);
@@ -284,6 +284,11 @@ static int check_i8(const char* what, int64_t M, int64_t N, int64_t K, fp8dp_dty
   if (M < 1 || N < 1 || K < 1 || M > (1 << 30) || N > (1 << 30) || K > FP8DP_INT8_MAX_K) {
     set_error("%s: M and N must be 1 .. 2^30 and K 1 .. %d (got %lld, %lld, %lld)", what,
               FP8DP_INT8_MAX_K, (long long)M, (long long)N, (long long)K);
+    return FP8DP_EINVAL;
+  }
+  // (tiles of 64 x 64 then count in 32 bits)
+  if (M * N > (int64_t)1 << 40) {
+    set_error("%s: M * N must be at most 2^40 (got %lld, %lld)", what, (long long)M, (long long)N);
     return FP8DP_EINVAL;
   }
   if (workspace_bytes < 0 || !aligned_to(workspace, 16)) {

@@ -51,7 +51,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_i8_few(I8Args g, const T* x) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int frow = lane & 15, fch = lane >> 4;
-  const int n0 = blockIdx.x * 16, K = g.K, M = g.M;
+  const int n0 = (g.first + (int)blockIdx.x) * 16, K = g.K, M = g.M;
   uint8_t* const ring = lds + wave * SL * SLOT;
 
   // what the epilogue needs, ahead of everything
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_i8_few_any(I8Args g) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int frow = lane & 15, fch = lane >> 4;
-  const int n0 = blockIdx.x * 16, K = g.K, M = g.M;
+  const int n0 = (g.first + (int)blockIdx.x) * 16, K = g.K, M = g.M;
 
   const int n = n0 + 4 * fch;
   const RawCols4 cols = load_cols4<T>(g, n);
@@ -274,16 +274,23 @@ static int launch_few(const char* what, const I8Args& g, const void* x, hipStrea
   constexpr size_t ring = (size_t)WAVES * SL * ((CAST ? 0 : AG) + 2) * 1024;
   static_assert(ring >= (size_t)WAVES * ((AG + 1) / 2) * 1024, "the joined sums fit the ring");
   const size_t bytes = ring + (CAST ? skinny_cast_bytes(g.M, g.K, sizeof(T), WAVES) : 0);
-  hipLaunchKernelGGL((k_i8_few<T, AG, WAVES, SL, CAST>), dim3((unsigned)((g.N + 15) / 16)),
-                     dim3(64 * WAVES), bytes, stream, g, static_cast<const T*>(x));
-  return check_launch(what);
+  return for_blocks((g.N + 15) / 16, [&](int first, unsigned count) {
+    I8Args part = g;
+    part.first = first;
+    hipLaunchKernelGGL((k_i8_few<T, AG, WAVES, SL, CAST>), dim3(count), dim3(64 * WAVES), bytes, stream,
+                       part, static_cast<const T*>(x));
+    return check_launch(what);
+  });
 }
 
 template <typename T, int MT>
 static int launch_few_any(const char* what, const I8Args& g, hipStream_t stream) {
-  hipLaunchKernelGGL((k_i8_few_any<T, MT, 8>), dim3((unsigned)((g.N + 15) / 16)), dim3(512), 0,
-                     stream, g);
-  return check_launch(what);
+  return for_blocks((g.N + 15) / 16, [&](int first, unsigned count) {
+    I8Args part = g;
+    part.first = first;
+    hipLaunchKernelGGL((k_i8_few_any<T, MT, 8>), dim3(count), dim3(512), 0, stream, part);
+    return check_launch(what);
+  });
 }
 
 template <typename T>

@@ -43,7 +43,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_i8_tile(I8Args g) {
 
   const int tiles_n = (g.N + BN - 1) / BN;
   const int ntiles = ((g.M + BM - 1) / BM) * tiles_n;
-  const int tile = tile_of_block(blockIdx.x, ntiles);
+  const int tile = tile_of_block(g.first + (int)blockIdx.x, ntiles);
   // bands 4 tiles wide: the 32 tiles that an XCD has in hand are 8 x 4, whose operands are 12
   // tiles in all, not 2 x 16
   const int tiles_m = (g.M + BM - 1) / BM, band = tile / (4 * tiles_m);
@@ -193,13 +193,12 @@ template <typename T, int WM, int WN, int TM, int TN, int S>
 static int launch_tile(const char* what, const I8Args& g, hipStream_t stream) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
   const int64_t tiles = (((int64_t)g.M + BM - 1) / BM) * (((int64_t)g.N + BN - 1) / BN);
-  if (tiles * 64 * WM * WN > 0xFFFFFFFF) {   // threads of a launch
-    set_error("%s: shape too large", what);
-    return FP8DP_EINVAL;
-  }
-  hipLaunchKernelGGL((k_i8_tile<T, WM, WN, TM, TN, S>), dim3((unsigned)tiles), dim3(64 * WM * WN),
-                     0, stream, g);
-  return check_launch(what);
+  return for_blocks(tiles, [&](int first, unsigned count) {
+    I8Args part = g;
+    part.first = first;
+    hipLaunchKernelGGL((k_i8_tile<T, WM, WN, TM, TN, S>), dim3(count), dim3(64 * WM * WN), 0, stream, part);
+    return check_launch(what);
+  });
 }
 
 int tile_i8(const char* what, fp8dp_dtype yt, const I8Args& g, bool wide, hipStream_t stream) {

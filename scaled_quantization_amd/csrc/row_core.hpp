@@ -403,8 +403,8 @@ __device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
   return s;
 }
 // Packs the codes of 8 values (bytes in order).  The row's amax is finite and not zero.
-// EXACT32: x has 32 bits, so p is rounded and a quotient may be as close to a half as
-// p's rounding error e: values next to a border (one in some thousands) are
+// EXACT32: x has 32 bits (FP32 tensors and a norm's values), so p is rounded and a quotient may be
+// as close to a half as p's rounding error e: values next to a border (one in some thousands) are
 // decided by the sign of |p - q m| + e - m / 2, whose terms are exact there.
 template <bool EXACT32>
 __device__ __forceinline__ uint2 codes8(const float x[8], const RowScale& s) {

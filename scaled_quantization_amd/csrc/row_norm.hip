@@ -230,7 +230,7 @@ __global__ __launch_bounds__(THR == 64 ? 256 : THR) void k_row(RowArgs a) {
       for (int i = 0; i < NV; ++i) {
         const int c = column(i);
         uint2 code = {0u, 0u};
-        if (plain) code = codes8<!NORM && sizeof(T) == 4>(v[i], s);
+        if (plain) code = codes8<NORM || sizeof(T) == 4>(v[i], s);
         // rows of q may be padded by up to 15 bytes of zeros
         if (i < NV - 1) store_codes8(element(q, c), 8, code);
         else store_codes8(q + c, a.ldq - c < 8 ? (int)(a.ldq - c) : 8, code);
@@ -328,7 +328,7 @@ __global__ __launch_bounds__(THR == 64 ? 256 : THR) void k_row_loop(RowArgs a) {
         if constexpr (NORM) normed(c);
         else load8(again + c, cols - c, w);
         uint2 code = {0u, 0u};
-        if (plain) code = codes8<!NORM && sizeof(T) == 4>(w, s);
+        if (plain) code = codes8<NORM || sizeof(T) == 4>(w, s);
         store_codes8(a.q + row * a.ldq + c, wide - c, code);
       }
     }

@@ -28,15 +28,14 @@ struct NormBwdArgs {
   float* parts;        // [workgroups][2][cols]
 };
 
-// h and g of one vector.  For inputs of 16 bits h is one fused multiply-add with -mean rstd,
-// whose rounding is far below the inputs' own; binary32 takes the difference first.
-template <typename T>
+// h and g of one vector.  h takes the difference first, whatever the type: a fused z rstd - mean rstd
+// would round mean rstd, which a row far from zero makes many times h, and dweight, which is
+// binary32, would show it.
 __device__ __forceinline__ void norm_hg(const float z[8], const float dy[8], const float w[8],
                                         float mean, float rstd, float h[8], float g[8]) {
-  const float shift = -mean * rstd;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    h[j] = sizeof(T) == 2 ? __builtin_fmaf(z[j], rstd, shift) : (z[j] - mean) * rstd;
+    h[j] = (z[j] - mean) * rstd;
     g[j] = dy[j] * w[j];
   }
 }
@@ -148,7 +147,7 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBwdWaves : THR) void k_norm_bwd(N
         mask.clear_empty(raw);
       }
       widen8f(raw, vd);
-      norm_hg<T>(vz, vd, w[i], r.mean, r.rstd, h, g);
+      norm_hg(vz, vd, w[i], r.mean, r.rstd, h, g);
     };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -243,7 +242,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_long(NormBwdArgs a) {
         load8(static_cast<const T*>(a.z) + at, n, z);
         load8(static_cast<const T*>(a.dy) + at, n, dy);
         load_param8<T>(a.weight, a.wf32, c, n, 1.0f, w);
-        norm_hg<T>(z, dy, w, mean, rstd, h, g);
+        norm_hg(z, dy, w, mean, rstd, h, g);
         if (pass == 0) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {

@@ -1,5 +1,5 @@
 """Where the operators around the MLP keep more than their outputs' own rounding (GPU): INT8 codes
-behind a norm.
+behind a norm, weight gradients of rows far from zero.
 
 U = 2^-24 is a binary32 rounding."""
 import numpy as np
@@ -53,3 +53,28 @@ def test_codes_behind_a_norm_are_those_of_its_values(rows, cols):
     top = v.abs().amax(1, keepdim=True)
     want = torch.round(v * 127.0 / top).to(torch.int8)       # 127 v is exact in 64 bits
     assert torch.equal(q, want), f"{int((q != want).sum())} of {q.numel()} codes differ"
+
+
+# ------------------------------------------------------------------ gradients of rows far from zero
+@pytest.mark.parametrize("cols", [7, 64, 768, 1001, 2048, 4096, 8192, 10000])
+@pytest.mark.parametrize("t, mean", [(torch.bfloat16, 40.0), (torch.float16, 340.0), (torch.float32, 5000.0)],
+                         ids=IDS)
+def test_weight_gradient_of_rows_with_a_distant_mean(t, mean, cols):
+    # h = (z - mean) rstd takes two roundings wherever the mean is; with the product's by dy and at
+    # most rows - 1 of the sum a column is off by (rows + 3) U of its terms' magnitudes, one more for second order
+    rows = 3
+    z, dy = draw((rows, cols), t, cols, 1.0, mean), draw((rows, cols), t, 2)
+    m = z.float().mean(1)
+    r = 1.0 / torch.sqrt(z.float().var(1, unbiased=False) + 1e-5)
+    dz, dw, db = torch.empty_like(z, device=DEV), torch.empty(cols, device=DEV), torch.empty(cols, device=DEV)
+    ws = torch.empty(2 * rows * cols, device=DEV)
+    sq.layer_norm_backward(dy.to(DEV), z.to(DEV), None, m.to(DEV), r.to(DEV), dz, dw, db, ws)
+    d = f64(dy)
+    h = (f64(z) - f64(m)[:, None]) * f64(r)[:, None]
+    close(dw, (d * h).sum(0), (rows + 4) * U * np.abs(d * h).sum(0), "dweight")
+    # a constant row is its own mean: no gradient of the weight at all
+    z.fill_(mean)
+    m.fill_(mean)
+    sq.layer_norm_backward(dy.to(DEV), z.to(DEV), None, m.to(DEV), torch.full((rows,), 316.0, device=DEV), dz, dw,
+                           db, ws)
+    assert (dw == 0).all()

@@ -338,6 +338,22 @@ __device__ __forceinline__ uint32_t row_umax(uint32_t x, uint32_t* scratch) {
   return x;
 }
 
+// A running sum of any length: what each addition rounds off is kept beside it (Knuth's exact
+// error of a sum), so the total is off by 2 roundings instead of one per term.  An infinity
+// or a NaN comes out as the plain sum's.
+struct LongSum {
+  float s = 0.0f, e = 0.0f;
+  __device__ __forceinline__ void add(float v) {
+    const float t = s + v, b = t - s;
+    e += (s - (t - b)) + (v - b);
+    s = t;
+  }
+  __device__ __forceinline__ float total() const { return e == e ? s + e : s; }
+};
+__device__ __forceinline__ float sum8(const float v[8]) {
+  return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+}
+
 // ------------------------------------------------------------------ dropout
 // Philox4x32 (Salmon et al., SC 2011), 10 rounds: per round two 32 x 32 -> 64
 // products and four XORs, the key advanced by the two Weyl constants.

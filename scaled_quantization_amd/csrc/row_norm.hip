@@ -240,7 +240,7 @@ __global__ __launch_bounds__(THR == 64 ? 256 : THR) void k_row(RowArgs a) {
 }
 
 // Rows of more than 16384 elements, or less than 8: a loop that reads the row
-// again for each statistic and for the output.
+// again for each statistic and for the output.  A thread's sums may be of 2^17 vectors: LongSum.
 template <typename T, int THR, bool DROP, bool NORM, bool QUANT>
 __global__ __launch_bounds__(THR == 64 ? 256 : THR) void k_row_loop(RowArgs a) {
   constexpr int RPB = THR == 64 ? 4 : 1;
@@ -262,7 +262,8 @@ __global__ __launch_bounds__(THR == 64 ? 256 : THR) void k_row_loop(RowArgs a) {
     float* const sc = scratch + (THR > 64 ? turn * 3 * WAVES : 0);
     const int64_t base = row * cols;
     const T* const again = (a.z != nullptr ? static_cast<const T*>(a.z) : x) + base;
-    float w[8], sum = 0.0f, mean = 0.0f, rstd = 0.0f;
+    float w[8], mean = 0.0f, rstd = 0.0f;
+    LongSum sum;
     uint32_t top = 0;
     auto normed = [&](int c) {
       float g[8], b[8];
@@ -289,24 +290,24 @@ __global__ __launch_bounds__(THR == 64 ? 256 : THR) void k_row_loop(RowArgs a) {
       }
       if constexpr (NORM) {
         zero_from8(n, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum += w[j];
+        sum.add(sum8(w));
       } else if constexpr (QUANT) {
         top = magnitude8(w, top);
       }
     }
     if constexpr (NORM) {
-      mean = row_sum<THR>(sum, sc) * inv_cols;
-      float sq = 0.0f;
+      mean = row_sum<THR>(sum.total(), sc) * inv_cols;
+      LongSum sq;
       for (int c = t * 8; c < cols; c += THR * 8) {
         load8(again + c, cols - c, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] -= mean;
         zero_from8(cols - c, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(w[j], w[j], sq);
+        for (int j = 0; j < 8; ++j) w[j] *= w[j];
+        sq.add(sum8(w));
       }
-      rstd = rsqrtf(row_sum<THR>(sq, sc + WAVES) * inv_cols + a.eps);
+      rstd = rsqrtf(row_sum<THR>(sq.total(), sc + WAVES) * inv_cols + a.eps);
       if (t == 0) {
         if (a.mean != nullptr) a.mean[row] = mean;
         if (a.rstd != nullptr) a.rstd[row] = rstd;

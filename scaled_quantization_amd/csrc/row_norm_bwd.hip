@@ -82,11 +82,19 @@ __device__ __forceinline__ void row_sum2(float& x, float& y, float* scratch) {
 
 constexpr int kBwdWaves = 4;   // waves of a workgroup whose waves own rows
 
+// Rows whose weight gradients a thread sums in registers before that sum joins those of its earlier
+// rows in its own words of LDS: 2^24 rows are two sums of 64 terms each, not one of 4096 whose
+// roundings fall to one side (dbias of nearly equal gradients was off by 400 roundings).
+constexpr int kBwdHeld = 64;
+
 // STREAM: tensors beyond the caches, read past them.
 template <typename T, int NV, int THR, bool DROP, bool STREAM>
 __global__ __launch_bounds__(THR == 64 ? 64 * kBwdWaves : THR) void k_norm_bwd(NormBwdArgs a) {
-  constexpr int RPB = THR == 64 ? kBwdWaves : 1;
-  __shared__ float lds[THR == 64 ? kBwdWaves / 2 * NV * 16 * 64 : 2 * 2 * (THR / 64)];
+  constexpr int RPB = THR == 64 ? kBwdWaves : 1, THREADS = RPB * THR;
+  // the weight gradients of earlier rows, [16 NV][thread], and the scratch of a row's sums
+  __shared__ float lds[NV * 16 * THREADS + (THR == 64 ? 0 : 2 * 2 * (THR / 64))];
+  float* const earlier = lds + threadIdx.x;
+  float* const scratch = lds + NV * 16 * THREADS;
   const int t = THR > 64 ? (int)threadIdx.x : (int)(threadIdx.x & 63);
   const int sub = THR > 64 ? 0 : (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cols = a.cols;
@@ -131,57 +139,81 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBwdWaves : THR) void k_norm_bwd(N
   }
 
   int turn = 0;
-  for (int64_t row = first; row < a.rows; row += step, turn ^= 1) {
-    const Row r = next;
-    load(row + step < a.rows ? row + step : row, next);
-    float sg = 0.0f, sgh = 0.0f;
-    // h and g of vector i (the compiler keeps them over the reduction where registers allow)
-    auto make = [&](int i, float* h, float* g, float* vd) {
-      float vz[8];
-      Raw8<T> raw = r.z[i];
-      if (i == NV - 1) settle(raw, n_last, ragged);
-      widen8f(raw, vz);
-      raw = r.dy[i];
-      if (i == NV - 1) {
-        settle(raw, n_last, ragged);
-        mask.clear_empty(raw);
-      }
-      widen8f(raw, vd);
-      norm_hg(vz, vd, w[i], r.mean, r.rstd, h, g);
-    };
+  bool more = false;   // there are sums of earlier rows
+  for (int64_t row = first;;) {
+    const int64_t stop = std::min(row + kBwdHeld * step, a.rows);
+    for (; row < stop; row += step, turn ^= 1) {
+      const Row r = next;
+      load(row + step < a.rows ? row + step : row, next);
+      float sg = 0.0f, sgh = 0.0f;
+      // h and g of vector i (the compiler keeps them over the reduction where registers allow)
+      auto make = [&](int i, float* h, float* g, float* vd) {
+        float vz[8];
+        Raw8<T> raw = r.z[i];
+        if (i == NV - 1) settle(raw, n_last, ragged);
+        widen8f(raw, vz);
+        raw = r.dy[i];
+        if (i == NV - 1) {
+          settle(raw, n_last, ragged);
+          mask.clear_empty(raw);
+        }
+        widen8f(raw, vd);
+        norm_hg(vz, vd, w[i], r.mean, r.rstd, h, g);
+      };
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float h[8], g[8], vd[8];
-      make(i, h, g, vd);
+      for (int i = 0; i < NV; ++i) {
+        float h[8], g[8], vd[8];
+        make(i, h, g, vd);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          sg += g[j];
+          sgh = __builtin_fmaf(g[j], h[j], sgh);
+          dw[i][j] = __builtin_fmaf(vd[j], h[j], dw[i][j]);
+          db[i][j] += vd[j];
+        }
+      }
+      row_sum2<THR>(sg, sgh, scratch + (THR > 64 ? turn * 2 * (THR / 64) : 0));
+      const float mg = sg * inv_cols, mgh = sgh * inv_cols;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int n = i < NV - 1 ? 8 : n_last;
+        float va[8] = {};
+        if (add != nullptr) {
+          Raw8<T> raw = r.add[i];
+          if (i == NV - 1) settle(raw, n_last, ragged);
+          widen8f(raw, va);
+        }
+        float h[8], g[8], vd[8];
+        make(i, h, g, vd);
+        if (i < NV - 1 || n > 0)
+          norm_out<T, DROP>(a, key, row, column(i) / 8, n, h, g, va, r.rstd, mg, mgh);
+      }
+    }
+    if (row >= a.rows) break;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        sg += g[j];
-        sgh = __builtin_fmaf(g[j], h[j], sgh);
-        dw[i][j] = __builtin_fmaf(vd[j], h[j], dw[i][j]);
-        db[i][j] += vd[j];
+        float *const ew = earlier + (i * 16 + j) * THREADS, *const eb = ew + 8 * THREADS;
+        *ew = more ? *ew + dw[i][j] : dw[i][j];
+        *eb = more ? *eb + db[i][j] : db[i][j];
+        dw[i][j] = db[i][j] = 0.0f;
       }
-    }
-    row_sum2<THR>(sg, sgh, lds + (THR > 64 ? turn * 2 * (THR / 64) : 0));
-    const float mg = sg * inv_cols, mgh = sgh * inv_cols;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int n = i < NV - 1 ? 8 : n_last;
-      float va[8] = {};
-      if (add != nullptr) {
-        Raw8<T> raw = r.add[i];
-        if (i == NV - 1) settle(raw, n_last, ragged);
-        widen8f(raw, va);
-      }
-      float h[8], g[8], vd[8];
-      make(i, h, g, vd);
-      if (i < NV - 1 || n > 0)
-        norm_out<T, DROP>(a, key, row, column(i) / 8, n, h, g, va, r.rstd, mg, mgh);
-    }
+    more = true;
   }
   if (!a.sums) return;
+  if (more) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dw[i][j] += earlier[(i * 16 + j) * THREADS];
+        db[i][j] += earlier[(i * 16 + 8 + j) * THREADS];
+      }
+  }
 
   if constexpr (THR == 64) {
-    // the waves' sums, halved in three steps through LDS (lane-major: no conflicts)
+    // the waves' sums, halved in two steps through LDS (lane-major: no conflicts)
 #pragma unroll
     for (int s = kBwdWaves / 2; s > 0; s >>= 1) {
       __syncthreads();
@@ -232,7 +264,8 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_long(NormBwdArgs a) {
   int turn = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
     const float mean = a.mean[row], rstd = a.rstd[row];
-    float sg = 0.0f, sgh = 0.0f, mg = 0.0f, mgh = 0.0f;
+    float mg = 0.0f, mgh = 0.0f;
+    LongSum sg, sgh;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
       for (int64_t c = (int64_t)t * 8; c < cols; c += 8192) {
@@ -244,11 +277,10 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_long(NormBwdArgs a) {
         load_param8<T>(a.weight, a.wf32, c, n, 1.0f, w);
         norm_hg(z, dy, w, mean, rstd, h, g);
         if (pass == 0) {
+          sg.add(sum8(g));
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            sg += g[j];
-            sgh = __builtin_fmaf(g[j], h[j], sgh);
-          }
+          for (int j = 0; j < 8; ++j) g[j] *= h[j];
+          sgh.add(sum8(g));
         } else {
           float add[8] = {};
           if (a.dz_add != nullptr) load8(static_cast<const T*>(a.dz_add) + at, n, add);
@@ -256,9 +288,11 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_long(NormBwdArgs a) {
         }
       }
       if (pass == 0) {
-        row_sum2<1024>(sg, sgh, lds + turn * 32);
-        mg = sg * inv_cols;
-        mgh = sgh * inv_cols;
+        mg = sg.total();
+        mgh = sgh.total();
+        row_sum2<1024>(mg, mgh, lds + turn * 32);
+        mg *= inv_cols;
+        mgh *= inv_cols;
       }
     }
   }
@@ -269,7 +303,7 @@ __global__ __launch_bounds__(256) void k_norm_bwd_cols(NormBwdArgs a) {
   const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   const int cols = a.cols, n = (int)(cols - c);
   if (c >= cols) return;
-  float dw[8] = {}, db[8] = {};
+  LongSum dw[8], db[8];
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     const float mean = a.mean[row], rstd = a.rstd[row];
     float z[8], dy[8];
@@ -277,13 +311,19 @@ __global__ __launch_bounds__(256) void k_norm_bwd_cols(NormBwdArgs a) {
     load8(static_cast<const T*>(a.dy) + row * cols + c, n, dy);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      dw[j] = __builtin_fmaf(dy[j], (z[j] - mean) * rstd, dw[j]);
-      db[j] += dy[j];
+      dw[j].add(dy[j] * ((z[j] - mean) * rstd));
+      db[j].add(dy[j]);
     }
   }
+  float sw[8], sb[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    sw[j] = dw[j].total();
+    sb[j] = db[j].total();
+  }
   float* const p = a.parts + (int64_t)blockIdx.y * 2 * cols;
-  store8(p + c, n, dw);
-  store8(p + cols + c, n, db);
+  store8(p + c, n, sw);
+  store8(p + cols + c, n, sb);
 }
 
 // dweight and dbias from `nparts` partial sums of 2 * cols values: 32 columns (a cache

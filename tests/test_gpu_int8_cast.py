@@ -40,3 +40,14 @@ def test_every_length_of_short_rows(t, M):
         w8, w_scale = codes_of(draw((40, K), t, K, 0.02))
         linear(many, many_w8, many_scale)
         check_linear(draw((M, K), t, K + 1), w8, w_scale, f"{M} tokens, K {K}")
+
+
+@pytest.mark.parametrize("t, M, K", [
+    # the longest rows that are cast in the product's launch, and the next ones, which are not
+    (torch.bfloat16, 1, 20480), (torch.bfloat16, 1, 20496), (torch.float16, 1, 20480), (torch.float16, 1, 20496),
+    (torch.float32, 1, 12288), (torch.float32, 1, 12304), (torch.bfloat16, 4, 4096), (torch.bfloat16, 4, 4112),
+    (torch.float16, 16, 1024), (torch.float16, 16, 1040), (torch.float32, 16, 768), (torch.float32, 16, 784),
+    (torch.float32, 7, 1744), (torch.float32, 7, 1760)])
+def test_longest_rows_that_are_cast_in_the_launch(t, M, K):
+    w8, w_scale = codes_of(draw((100, K), t, 2, 0.02))
+    check_linear(draw((M, K), t, 1), w8, w_scale, f"{M} tokens, K {K}")

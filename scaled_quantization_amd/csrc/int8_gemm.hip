@@ -29,10 +29,14 @@ constexpr int64_t kSplitBytes = (int64_t)16 << 20;
 // They are issued without a branch (a chunk past K is read as the row's last 16 bytes and
 // cleared when it is put into LDS), or the compiler would have to wait for all of them.
 // TINY: rows of less than 16 bytes, in one stage.
-// gridDim.y > 1: workgroup (t, s) takes the s-th range of stages and leaves its integer sums in
+// gridDim.y > 1 (SPLIT): workgroup (t, s) takes the s-th range of stages and leaves its integer sums in
 // `partial`, [range][tile][4 registers][thread], for k_i8_join.
+template <int TW, bool TINY>
+constexpr bool kSplits = TW == 1 && !TINY;   // larger tiles are for many of them, tiny rows are one stage
+
 template <typename T, int TW, int PF, bool TINY>
 __global__ __launch_bounds__(256) void k_i8_any(I8Args g, v4i_t* partial) {
+  constexpr bool SPLIT = kSplits<TW, TINY>;
   constexpr int R = 64 * TW, TILE = R * kBK, L = R / 32;   // rows, bytes of a tile, chunks per thread
   __shared__ __attribute__((aligned(16))) uint8_t lds[4 * TILE];
   __shared__ TileScales<R, R> scales;
@@ -44,8 +48,8 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args g, v4i_t* partial) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = (wave >> 1) * 32 * TW, wn = (wave & 1) * 32 * TW;
   const int stages = (g.K + kBK - 1) / kBK;
-  const int first = (int)((int64_t)stages * blockIdx.y / gridDim.y);
-  const int turns = (int)((int64_t)stages * (blockIdx.y + 1) / gridDim.y) - first;
+  const int first = SPLIT ? (int)((int64_t)stages * blockIdx.y / gridDim.y) : 0;
+  const int turns = SPLIT ? (int)((int64_t)stages * (blockIdx.y + 1) / gridDim.y) - first : stages;
 
   // thread t moves chunk t % 8 of rows t / 8 + 32 i of both tiles
   const int srow = tid >> 3, sch = tid & 7;
@@ -95,7 +99,7 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args g, v4i_t* partial) {
   // PF later
 #pragma unroll
   for (int u = 0; u < PF; ++u) load(u, first + u);
-  if (gridDim.y == 1) load_scales<T>(g, scales, m0, n0, tid, 256);
+  if (!SPLIT || gridDim.y == 1) load_scales<T>(g, scales, m0, n0, tid, 256);
   put(0, 0, 0);
   load(0, first + PF);
   __syncthreads();
@@ -122,43 +126,41 @@ __global__ __launch_bounds__(256) void k_i8_any(I8Args g, v4i_t* partial) {
   };
   for (int t = 0; t < turns; t += PF)
     static_for<PF>([&](auto U) { turn(t + decltype(U)::value, (decltype(U)::value + 1) % PF); });
-  if (gridDim.y > 1) {
-    v4i_t* const o = partial + ((int64_t)blockIdx.y * ntiles + tile) * (TW * TW * 4 * 256) + tid;
+  if constexpr (SPLIT) {
+    if (gridDim.y > 1) {
+      v4i_t* const o = partial + ((int64_t)blockIdx.y * ntiles + tile) * (4 * 256) + tid;
 #pragma unroll
-    for (int i = 0; i < TW * TW * 4; ++i) {
-      const v16i_t& c = acc[i / (4 * TW)][i / 4 % TW];
-      const int q = 4 * (i % 4);
-      o[i * 256] = v4i_t{c[q], c[q + 1], c[q + 2], c[q + 3]};
+      for (int i = 0; i < 4; ++i) {
+        const v16i_t& c = acc[0][0];
+        o[i * 256] = v4i_t{c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]};
+      }
+      return;
     }
-    return;
   }
   turn_out<T>(g, acc, lds + wave * 32 * TW * 128, scales, m0, n0, wm, wn, lane);
 }
 
-// Joins the ranges' sums of a tile and writes its outputs.
-template <typename T, int TW>
+// Joins the ranges' sums of a tile of 64 x 64 and writes its outputs.
+template <typename T>
 __global__ __launch_bounds__(256) void k_i8_join(I8Args g, const v4i_t* partial, int ranges) {
-  constexpr int R = 64 * TW;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * 32 * TW * 128];
-  __shared__ TileScales<R, R> scales;
-  const int tiles_n = (g.N + R - 1) / R, tile = blockIdx.x;
-  const int m0 = (tile / tiles_n) * R, n0 = (tile % tiles_n) * R;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * 32 * 128];
+  __shared__ TileScales<64, 64> scales;
+  const int tiles_n = (g.N + 63) / 64, tile = blockIdx.x;
+  const int m0 = (tile / tiles_n) * 64, n0 = (tile % tiles_n) * 64;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   load_scales<T>(g, scales, m0, n0, tid, 256);
-  v16i_t acc[TW][TW];
+  v16i_t acc[1][1];
 #pragma unroll
-  for (int i = 0; i < TW * TW * 4; ++i) {
+  for (int i = 0; i < 4; ++i) {
     v4i_t sum = {};
-    const v4i_t* p = partial + ((int64_t)tile * TW * TW * 4 + i) * 256 + tid;
+    const v4i_t* p = partial + ((int64_t)tile * 4 + i) * 256 + tid;
 #pragma unroll 4
-    for (int s = 0; s < ranges; ++s, p += (int64_t)gridDim.x * (TW * TW * 4 * 256)) sum += *p;
-    v16i_t& c = acc[i / (4 * TW)][i / 4 % TW];
+    for (int s = 0; s < ranges; ++s, p += (int64_t)gridDim.x * (4 * 256)) sum += *p;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) c[4 * (i % 4) + r] = sum[r];
+    for (int r = 0; r < 4; ++r) acc[0][0][4 * i + r] = sum[r];
   }
   __syncthreads();
-  turn_out<T>(g, acc, lds + wave * 32 * TW * 128, scales, m0, n0, (wave >> 1) * 32 * TW,
-              (wave & 1) * 32 * TW, lane);
+  turn_out<T>(g, acc, lds + wave * 32 * 128, scales, m0, n0, (wave >> 1) * 32, (wave & 1) * 32, lane);
 }
 
 template <typename T, int TW, int PF, bool TINY = false>
@@ -168,7 +170,7 @@ static int launch_any(const char* what, const I8Args& g, void* workspace, int64_
                         (((int64_t)g.N + 64 * TW - 1) / (64 * TW));
   // K in ranges of at least 4 stages, as long as there are compute units without a tile
   int64_t ranges = 1;
-  if (TW == 1 && !TINY) {
+  if constexpr (kSplits<TW, TINY>) {
     const int64_t stages = (g.K + kBK - 1) / kBK, bytes = tiles * 64 * 64 * 4;
     ranges = std::min({stages / 4, num_cus() / tiles, std::min(workspace_bytes, kSplitBytes) / bytes,
                        (int64_t)16});
@@ -184,10 +186,13 @@ static int launch_any(const char* what, const I8Args& g, void* workspace, int64_
                        part, partial);
     return check_launch(what);
   });
-  if (rc || ranges == 1) return rc;
-  hipLaunchKernelGGL((k_i8_join<T, TW>), dim3((unsigned)tiles), dim3(256), 0, stream, g, partial,
-                     (int)ranges);
-  return check_launch(what);
+  if constexpr (kSplits<TW, TINY>) {
+    if (rc || ranges == 1) return rc;
+    hipLaunchKernelGGL((k_i8_join<T>), dim3((unsigned)tiles), dim3(256), 0, stream, g, partial,
+                       (int)ranges);
+    return check_launch(what);
+  }
+  return rc;
 }
 
 // Rows of K bytes at any alignment -> rows of ld bytes, a multiple of 16, zeros behind K.

@@ -25,14 +25,15 @@ def rel(a, b):
     return float((a - b).norm() / b.norm())
 
 
-def training(tokens=2048, width=768, p=0.1, seed=1234, step=7):
+def training(tokens=2048, width=768, p=0.1, seed=1234, step=7, layer=3, layers=12):
     """One step of the MLP's tail; returns the errors of z, y and the gradients."""
     g = torch.Generator(device=DEV).manual_seed(1)
     bf = lambda *s, std=1.0: (torch.randn(s, generator=g, device=DEV) * std).bfloat16()
     mlp, residual, dy, dz_next = bf(tokens, width), bf(tokens, width, std=2.0), bf(tokens, width), bf(tokens, width)
     weight, bias = 1.0 + bf(width, std=0.1), bf(width, std=0.1)
 
-    rng = torch.tensor([seed, step], dtype=torch.int64, device=DEV)      # a step's offset, e.g. its number
+    # seed and offset: the same two words give the same mask, so every layer of every step has its own
+    rng = torch.tensor([seed, step * layers + layer], dtype=torch.int64, device=DEV)
     z, y, dz, dmlp = (torch.empty_like(mlp) for _ in range(4))
     mean, rstd = (torch.empty(tokens, device=DEV) for _ in range(2))
     sq.dropout_add_layer_norm(mlp, residual, p, rng, weight, bias, EPS, z, y, mean, rstd)

@@ -60,7 +60,10 @@ int layer_norm(const void* x, const void* weight, const void* bias, int64_t rows
    the gradient of out, with the same p and rng and no residual, is the
    backward pass.
    rng: two 64-bit words on the device, seed and offset, read by the kernel (a
-   captured graph may change them between replays); NULL only with p = 0.
+   captured graph may change them between replays); NULL only with p = 0.  The words
+   alone decide the mask: two uses with the same words drop the same elements,
+   so each layer, step and rank has its own (the offset step * layers + layer, say, and a
+   seed per rank), and a backward pass those of its forward.
    out may be x or residual.  A dropped element contributes +0, also where x is
    not finite.
    Errors: EINVAL for a NULL x or out, rows or cols out of range, an unknown

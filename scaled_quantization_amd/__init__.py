@@ -676,7 +676,8 @@ def layer_norm_backward(dy: torch.Tensor, z: torch.Tensor, weight, mean: torch.T
 
 def dropout_add(x: torch.Tensor, residual, p: float, rng, out: torch.Tensor, stream=None) -> None:
     """out = residual + keep x / (1 - p) (residual None: no sum); rng: [seed, offset], two
-    64-bit integers on the device.  The same call on the gradient is the backward pass."""
+    64-bit integers on the device, which alone decide the mask: each layer and step has its own.
+    The same call on the gradient is the backward pass."""
     dt = _dtype(x, "dropout_add: x")
     x_shape = x.shape
     rows, cols = _last(x, x_shape, "dropout_add: x")

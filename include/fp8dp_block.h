@@ -13,7 +13,8 @@
  * inputs, except where a call says so.
  *
  * Sums, statistics and the norm's arithmetic are binary32 (integers for the
- * INT8 product); each output is rounded once, to its own type.
+ * INT8 product); long sums are joined so that their error hardly grows with
+ * their length.  Each output is rounded once, to its own type.
  */
 #ifndef FP8DP_BLOCK_H
 #define FP8DP_BLOCK_H

@@ -25,7 +25,9 @@ constexpr int64_t kSplitBytes = (int64_t)16 << 20;
 // any alignment into registers, then into double-buffered LDS tiles of 128 bytes of K
 // (the layout of gemm_core.hpp).  Four waves own TW x TW tiles of 32 x 32 each.
 // PF stages are in flight in registers: a stage's loads take microseconds to arrive, its
-// products a fraction of one (777 x 1023 x 1001: one stage ahead 14 us, four ahead 8.2).
+// products a fraction of one.  Four ahead against one (in a graph): operands from memory 128 x 2048 x 4096
+// 12.5 / 13.3 us, 777 x 1023 x 1001 9.4 / 9.1, 300 x 2049 x 640 7.6 / 6.7; from cache 12.1 / 11.8,
+// 8.3 / 7.7 and 6.7 / 5.5: the depth serves long rows only.
 // They are issued without a branch (a chunk past K is read as the row's last 16 bytes and
 // cleared when it is put into LDS), or the compiler would have to wait for all of them.
 // TINY: rows of less than 16 bytes, in one stage.
@@ -229,7 +231,8 @@ static int pad_rows(const char* what, const int8_t* src, int64_t ld_src, int K, 
 
 // Which tiles, from what a product with K = 4096 takes per round of workgroups (us, measured):
 // 256 x 256 one workgroup per compute unit, 64; 128 x 128 two, 40 (one alone 26; with rows at any
-// byte 62 and 25); 64 x 64 four, 57 (one 13, two 22).
+// byte 62 and 25); 64 x 64 four, 57 (one 13, two 22).  K scales all of them alike and leaves the ranking:
+// what a tile costs beside K (prologue, epilogue) is not in it, nor was it measured below K = 500 or N = 100.
 struct TileCost {
   double c256, c128, c64, c128_any;
   explicit TileCost(const I8Args& g) {

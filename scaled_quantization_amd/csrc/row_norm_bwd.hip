@@ -5,11 +5,12 @@
 //   dz = rstd (g - mean(g) - h mean(g h)) + dz_add,  dx = keep dz / (1 - p)
 //   dw = sum over rows of dy h,  db = sum over rows of dy
 //
-// One pass: a persistent grid walks the rows, a wave or workgroup per row as in
-// the forward kernels, and each thread keeps the weight gradients of its own
-// columns in registers over all its rows.  The partial sums of a workgroup
-// go to the workspace once, and a second kernel adds them in a fixed order (no
-// atomics, so the same call gives the same bits).  dy and z are read once.
+// Rows of 8 to 8192 elements in one pass, which reads dy and z once: a persistent grid walks the rows,
+// a wave or workgroup per row as in the forward kernels, and each thread keeps the weight
+// gradients of its own columns over all its rows.  The partial sums of a workgroup go to the
+// workspace once, and a second kernel adds them in a fixed order (no atomics, so the same
+// call gives the same bits).  Other rows are read three times: by a kernel for the weight
+// gradients, and twice by one for dz.
 #include <hip/hip_runtime.h>
 
 #include "row_core.hpp"
@@ -379,8 +380,8 @@ static int launch_bwd_as(const NormBwdArgs& a, float* dweight, float* dbias, hip
   constexpr int RPB = THR == 64 ? kBwdWaves : 1;
   // A compute unit gets waves for 16 vectors of a row and no more: each has two rows of loads in
   // flight, and more of them only spread the reads and writes over more of memory (per
-  // compute unit 8 waves of 2 vectors against 12: 65536 x 4096 270 / 298 us, 262144 x 768
-  // 201 / 208, 16384 x 768 20.0 / 21.7; 16 waves of 1 against 8: 30001 x 1600 60 / 68).  All are
+  // compute unit 8 waves of 2 vectors against 12: 65536 x 4096 270 / 303 us, 262144 x 768
+  // 200 / 207, 16384 x 768 19.9 / 21.6; 16 waves of 1 against 8: 30001 x 1600 60 / 70).  All are
   // resident at once and walk the same number of rows.
   static const int resident = [] {
     int n = 0;
@@ -399,8 +400,8 @@ static int launch_bwd_as(const NormBwdArgs& a, float* dweight, float* dbias, hip
 }
 
 // Beyond the 256 MB of the last-level cache: read past the caches (measured, with and without:
-// 65536 x 4096 271 / 290 us, 262144 x 768 198 / 213; 16384 x 768, which they hold, 21.1 / 20.4
-// and with dropout and residual 31.0 / 28.2).
+// 65536 x 4096 270 / 286 us, 262144 x 768 199 / 214; 16384 x 768, which they hold, 20.9 / 20.3
+// and with dropout and residual 31.2 / 28.5).
 template <typename T, int NV, int THR, bool DROP>
 static int launch_bwd(const NormBwdArgs& a, float* dweight, float* dbias, hipStream_t stream) {
   const int64_t tensors = 3 + (a.dz_add != nullptr) + (a.dx != nullptr);
@@ -437,8 +438,11 @@ static int launch_bwd_width(const NormBwdArgs& a, float* dweight, float* dbias,
   if (nvec <= 128) return launch_bwd<T, 2, 64, DROP>(a, dweight, dbias, stream);
   if (nvec <= 256) return launch_bwd<T, 1, 256, DROP>(a, dweight, dbias, stream);
   if (nvec <= 512) return launch_bwd<T, 2, 256, DROP>(a, dweight, dbias, stream);
+  // 128 registers a thread: 8 to 56 bytes a thread go to scratch with dropout, 12 in FP32, and it is
+  // still the better side (against the two kernels below: 4096 x 8192 46 / 97 us, with dropout and
+  // residual 71 / 116, FP32 84 / 149 and 157 / 195; 1024 x 4104 16 / 29)
   if (nvec <= 1024) return launch_bwd<T, 1, 1024, DROP>(a, dweight, dbias, stream);
-  // two vectors per thread of 1024 spill (128 registers a thread): 4096 x 16384 took 243 us, this 157
+  // two vectors per thread of 1024 spill all through: 4096 x 16384 took 299 us, this 155
   return launch_bwd_long<T, DROP>(a, dweight, dbias, stream);
 }
 

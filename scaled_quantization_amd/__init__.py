@@ -1,7 +1,7 @@
 """scaled_quantization_amd -- scaled FP8 quantization for an MLP down-projection on MI355X.
 
 A thin ctypes binding over ``libfp8dp.so`` (C ABI declared in
-``include/fp8dp.h`` and ``include/fp8dp_block.h``).  Every step of the path runs in the library's HIP
+``include/fp8dp.h``, ``include/fp8dp_block.h`` and ``include/fp8dp_gated.h``).  Every step of the path runs in the library's HIP
 kernels; this module only marshals torch device tensors into pointers, sizes
 and the current HIP stream, and turns nonzero return codes into exceptions.
 It raises if the library has not been built; there is no CPU fallback.
@@ -17,6 +17,9 @@ Operators around the MLP (include/fp8dp_block.h):
     layer_norm, layer_norm_backward, dropout_add, dropout_add_layer_norm,
     quantize_int8, layer_norm_quantize_int8, int8_gemm, int8_linear,
     int8_linear_workspace.
+The gated feed-forward block (include/fp8dp_gated.h):
+    gated_linear, gated_linear_backward, their _workspace sizes, block_norm, block_norm_backward,
+    lora_plan, lora_plan_size, lora_add, lora_add_workspace.
 """
 from __future__ import annotations
 
@@ -37,6 +40,8 @@ ACC_SLOTS = 64
 STATE_BYTES = 4288
 NORM_PARTS = 1024        # layer_norm_backward's workspace: 2 * min(rows, NORM_PARTS) * cols floats
 INT8_MAX_K = 131071
+(GATE_SILU, GATE_GELU, GATE_GELU_TANH, GATE_SIGMOID, GATE_RELU, GATE_RELU2,
+ GATE_IDENTITY) = range(7)    # activations of gated_linear
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp8dp.so")
@@ -93,6 +98,22 @@ _SIGS = {
     "int8_linear_workspace": ([_i64, _i64], _i64),
     "int8_linear": ([_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _i64, _vp],
                     ctypes.c_int),
+    "gated_linear_workspace": ([_i64, _i64, _i64], _i64),
+    "gated_linear": ([_vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _vp],
+                     ctypes.c_int),
+    "gated_linear_backward_workspace": ([_i64, _i64, _i64], _i64),
+    "gated_linear_backward": ([_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp,
+                               _vp, _vp, _i64, _vp], ctypes.c_int),
+    "block_norm": ([_vp, _vp, _vp, _vp, _i32, _vp, _i64, _i64, _i32, _i32, _i32, _f32, _f32, _f32,
+                    _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "block_norm_backward": ([_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i64, _i64, _i32,
+                             _i32, _i32, _f32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+                            ctypes.c_int),
+    "lora_plan_size": ([_i64, _i64], _i64),
+    "lora_plan": ([_vp, _i64, _i64, _vp, _vp], ctypes.c_int),
+    "lora_add_workspace": ([_i64, _i64, _i64, _i64, _i64], _i64),
+    "lora_add": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i32, _vp, _vp,
+                  _i64, _vp], ctypes.c_int),
     "fp8dp_last_error": ([], ctypes.c_char_p),
     "fp8dp_bench_act_bf16": ([_vp, _i64, _i32, _vp, _vp], ctypes.c_int),
     "fp8dp_bench_amax": ([_vp, _i64, _vp, _vp], ctypes.c_int),
@@ -796,6 +817,204 @@ def int8_linear(x: torch.Tensor, w8: torch.Tensor, w_scale: torch.Tensor, y: tor
     x, w8, w_scale, bias, y, workspace, s = _args(stream, x, w8, w_scale, bias, y, workspace)
     _check(lib().int8_linear(x, w8, w_scale, bias, M, N, K, yt, bt, y, workspace, room, s),
            "int8_linear")
+
+
+# --------------------------------------------------------------------------- gated feed-forward block
+def _bytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def gated_linear_workspace(M: int, N: int, K: int) -> int:
+    """Bytes of workspace with which gated_linear splits K where there are few tiles; may be 0."""
+    return lib().gated_linear_workspace(M, N, K)
+
+
+def _gated(name: str, x, w_gate, w_up, outs) -> tuple:
+    """(M, N, K, type code) of x [..., K] and w_gate, w_up [N, K]; outs: tensors [..., N] of x's type."""
+    dt = _dtype(x, f"{name}: x")
+    shape = x.shape
+    M, K = _last(x, shape, f"{name}: x")
+    if w_gate.dim() != 2 or w_gate.shape[1] != K:
+        raise Fp8dpError(f"{name}: weights must be [N, {K}], got {tuple(w_gate.shape)}")
+    N = w_gate.shape[0]
+    _like(w_gate, x.dtype, w_gate.shape, f"{name}: w_gate")
+    _like(w_up, x.dtype, w_gate.shape, f"{name}: w_up")
+    for what, t in outs:
+        if t is not None:
+            _like(t, x.dtype, shape[:-1] + (N,), f"{name}: {what}")
+    return M, N, K, dt
+
+
+def gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: int,
+                 h: torch.Tensor, gate=None, up=None, workspace=None, stream=None) -> None:
+    """h [..., N] = f(x w_gate^T) * (x w_up^T) for x [..., K] and weights [N, K], bfloat16 or
+    float16; act: GATE_SILU, ...; gate, up: the two products, for the backward pass.  workspace
+    (any contiguous tensor of gated_linear_workspace bytes, 16-byte aligned) lets K be split
+    where h is small."""
+    M, N, K, dt = _gated("gated_linear", x, w_gate, w_up, (("h", h), ("gate", gate), ("up", up)))
+    room = _bytes(workspace)
+    x, w_gate, w_up, h, gate, up, workspace, s = _args(stream, x, w_gate, w_up, h, gate, up, workspace)
+    _check(lib().gated_linear(x, w_gate, w_up, M, N, K, dt, act, h, gate, up, workspace, room, s),
+           "gated_linear")
+
+
+def gated_linear_backward_workspace(M: int, N: int, K: int) -> int:
+    """Bytes of workspace that gated_linear_backward needs."""
+    return lib().gated_linear_backward_workspace(M, N, K)
+
+
+def gated_linear_backward(dh: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, x: torch.Tensor,
+                          w_gate: torch.Tensor, w_up: torch.Tensor, act: int, workspace: torch.Tensor,
+                          dx=None, dw_gate=None, dw_up=None, stream=None) -> None:
+    """Gradients of gated_linear from dh and the forward's gate and up: dx, and dw_gate with
+    dw_up, all of x's type.  workspace: at least gated_linear_backward_workspace(M, N, K) bytes."""
+    name = "gated_linear_backward"
+    M, N, K, dt = _gated(name, x, w_gate, w_up, (("dh", dh), ("gate", gate), ("up", up)))
+    _like(dx, x.dtype, x.shape, f"{name}: dx")
+    _like(dw_gate, x.dtype, w_gate.shape, f"{name}: dw_gate")
+    _like(dw_up, x.dtype, w_gate.shape, f"{name}: dw_up")
+    room = _bytes(workspace)
+    dh, gate, up, x, w_gate, w_up, dx, dw_gate, dw_up, workspace, s = _args(
+        stream, dh, gate, up, x, w_gate, w_up, dx, dw_gate, dw_up, workspace)
+    _check(lib().gated_linear_backward(dh, gate, up, x, w_gate, w_up, M, N, K, dt, act, dx, dw_gate,
+                                       dw_up, workspace, room, s), name)
+
+
+def _gate_kind(gate, x_shape: torch.Size, x_dtype: torch.dtype, cols: int, what: str) -> tuple:
+    """(whether a gate has a value per token, its type code): [cols] of x's type or float32, or
+    x's shape and type."""
+    if gate is None:
+        return 0, _DTYPES[x_dtype]
+    if gate.dim() == 1 and len(x_shape) > 1:
+        return 0, _params((gate,), x_dtype, cols, what)
+    _like(gate, x_dtype, x_shape, what)
+    return 1, _DTYPES[x_dtype]
+
+
+def block_norm(x, residual: torch.Tensor, post_weight, gate, pre_weight, eps: float, z, y,
+               post_rstd=None, pre_rstd=None, residual_scale: float = 1.0,
+               branch_scale: float = 1.0, stream=None) -> None:
+    """From one block to the next: z = residual_scale residual + branch_scale gate rms(x) post_weight
+    and y = rms(z) pre_weight, rms(v) = v / sqrt(mean(v^2) + eps) over the last dimension.
+    gate: [cols] (for an x of two dimensions or more), x's shape, or None; x None: y =
+    rms(residual) pre_weight; y None: z alone.  Weights of x's type or float32 (None: ones);
+    post_rstd, pre_rstd: float32, one value per row, for the backward pass."""
+    dt = _dtype(residual, "block_norm: residual")
+    t, shape = residual.dtype, residual.shape
+    rows, cols = _last(residual, shape, "block_norm: residual")
+    _like(x, t, shape, "block_norm: x")
+    _like(z, t, shape, "block_norm: z")
+    _like(y, t, shape, "block_norm: y")
+    wt = _params((post_weight, pre_weight), t, cols, "block_norm: post_weight, pre_weight")
+    token, gt = _gate_kind(gate, shape, t, cols, "block_norm: gate")
+    _floats(post_rstd, rows, "block_norm: post_rstd")
+    _floats(pre_rstd, rows, "block_norm: pre_rstd")
+    x, residual, post_weight, gate, pre_weight, z, y, post_rstd, pre_rstd, s = _args(
+        stream, x, residual, post_weight, gate, pre_weight, z, y, post_rstd, pre_rstd)
+    _check(lib().block_norm(x, residual, post_weight, gate, token, pre_weight, rows, cols, dt, wt, gt,
+                            residual_scale, branch_scale, eps, z, y, post_rstd, pre_rstd, s),
+           "block_norm")
+
+
+def block_norm_backward(dy, dz_add, x, z, post_weight, gate, pre_weight, post_rstd, pre_rstd,
+                        dresidual: torch.Tensor, dx=None, dgate=None, dpost_weight=None,
+                        dpre_weight=None, workspace=None, residual_scale: float = 1.0,
+                        branch_scale: float = 1.0, stream=None) -> None:
+    """Gradients of block_norm from dy, dz_add (what reaches z past the second norm) and the
+    forward's x, z and statistics: dresidual, dx, dgate (float32 [cols] for a gate per channel, else
+    the gate's shape and type), dpost_weight and dpre_weight (float32; with a sum over rows
+    workspace, float32 of 2 * min(rows, NORM_PARTS) * cols values).  dy None: there was no y; x None:
+    there was no x (z is then the normed residual)."""
+    name = "block_norm_backward"
+    dt = _dtype(dresidual, f"{name}: dresidual")
+    t, shape = dresidual.dtype, dresidual.shape
+    rows, cols = _last(dresidual, shape, f"{name}: dresidual")
+    for what, v in (("dy", dy), ("dz_add", dz_add), ("x", x), ("z", z), ("dx", dx)):
+        _like(v, t, shape, f"{name}: {what}")
+    wt = _params((post_weight, pre_weight), t, cols, f"{name}: post_weight, pre_weight")
+    token, gt = _gate_kind(gate, shape, t, cols, f"{name}: gate")
+    for what, v, n in (("post_rstd", post_rstd, rows), ("pre_rstd", pre_rstd, rows),
+                       ("dpost_weight", dpost_weight, cols), ("dpre_weight", dpre_weight, cols)):
+        _floats(v, n, f"{name}: {what}")
+    if token:
+        _like(dgate, t, shape, f"{name}: dgate")
+    else:
+        _floats(dgate, cols, f"{name}: dgate")
+    need = 2 * min(rows, NORM_PARTS) * cols
+    if workspace is not None and (workspace.dtype is not _F32 or workspace.numel() < need) and not (
+            dpost_weight is None and dpre_weight is None and (dgate is None or token)):
+        raise Fp8dpError(f"{name}: workspace needs 2 * min(rows, {NORM_PARTS}) * cols = {need} float32")
+    (dy, dz_add, x, z, post_weight, gate, pre_weight, post_rstd, pre_rstd, dresidual, dx, dgate,
+     dpost_weight, dpre_weight, workspace, s) = _args(
+        stream, dy, dz_add, x, z, post_weight, gate, pre_weight, post_rstd, pre_rstd, dresidual, dx,
+        dgate, dpost_weight, dpre_weight, workspace)
+    _check(lib().block_norm_backward(dy, dz_add, x, z, post_weight, gate, token, pre_weight, post_rstd,
+                                     pre_rstd, rows, cols, dt, wt, gt, residual_scale, branch_scale,
+                                     dresidual, dx, dgate, dpost_weight, dpre_weight, workspace, s), name)
+
+
+def _int32(t: torch.Tensor, n: int, what: str) -> None:
+    if t.dtype is not torch.int32 or t.numel() != n:
+        raise Fp8dpError(f"{what}: expected {n} int32 values, got {t.dtype} {tuple(t.shape)}")
+
+
+def lora_plan_size(tokens: int, adapters: int) -> int:
+    """int32 values of a plan."""
+    size = lib().lora_plan_size(tokens, adapters)
+    if size < 0:
+        raise Fp8dpError(f"lora_plan_size: {tokens} tokens or {adapters} adapters out of range")
+    return size
+
+
+def lora_plan(index: torch.Tensor, adapters: int, plan: torch.Tensor, stream=None) -> None:
+    """Groups a step's tokens by adapter: index [tokens] int32, an index outside 0 .. adapters - 1
+    stands for no adapter; plan: lora_plan_size(tokens, adapters) int32 values, for any number of
+    lora_add calls."""
+    tokens = index.numel()
+    _int32(index, tokens, "lora_plan: index")
+    if tokens:
+        _int32(plan, lora_plan_size(tokens, adapters), "lora_plan: plan")
+    index, plan, s = _args(stream, index, plan)
+    _check(lib().lora_plan(index, tokens, adapters, plan, s), "lora_plan")
+
+
+def lora_add_workspace(tokens: int, N: int, K: int, rank: int, adapters: int) -> int:
+    """Bytes of workspace that lora_add needs."""
+    size = lib().lora_add_workspace(tokens, N, K, rank, adapters)
+    if size < 0:
+        raise Fp8dpError(f"lora_add_workspace: sizes out of range: {tokens} tokens, N {N}, K {K}, "
+                         f"rank {rank}, {adapters} adapters")
+    return size
+
+
+def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor,
+             plan: torch.Tensor, base, y: torch.Tensor, workspace: torch.Tensor, ranks=None,
+             stream=None) -> None:
+    """y [..., N] = base + scale[i] b[i] (a[i] x) for x [..., K], each token with the adapter i of
+    the plan: a [adapters, rank, K], b [adapters, N, rank], bfloat16 or float16; scale float32, ranks
+    int32 (or None: all of rank), one per adapter.  base None: zeros; y may be base.  workspace: at
+    least lora_add_workspace(tokens, N, K, rank, adapters) bytes."""
+    dt = _dtype(x, "lora_add: x")
+    t, shape = x.dtype, x.shape
+    tokens, K = _last(x, shape, "lora_add: x")
+    if a.dim() != 3 or b.dim() != 3:
+        raise Fp8dpError("lora_add: a must be [adapters, rank, K] and b [adapters, N, rank]")
+    adapters, rank = a.shape[:2]
+    N = b.shape[1]
+    _like(a, t, (adapters, rank, K), "lora_add: a")
+    _like(b, t, (adapters, N, rank), "lora_add: b")
+    _like(base, t, shape[:-1] + (N,), "lora_add: base")
+    _like(y, t, shape[:-1] + (N,), "lora_add: y")
+    _floats(scale, adapters, "lora_add: scale")
+    if ranks is not None:
+        _int32(ranks, adapters, "lora_add: ranks")
+    if tokens and adapters:
+        _int32(plan, lora_plan_size(tokens, adapters), "lora_add: plan")
+    room = _bytes(workspace)
+    x, a, b, scale, ranks, plan, base, y, workspace, s = _args(
+        stream, x, a, b, scale, ranks, plan, base, y, workspace)
+    _check(lib().lora_add(x, a, b, scale, ranks, plan, base, tokens, N, K, rank, adapters, dt, y,
+                          workspace, room, s), "lora_add")
 
 
 def fp8dp_bench_act_bf16(h: torch.Tensor, act: int, out: torch.Tensor, stream=None) -> None:

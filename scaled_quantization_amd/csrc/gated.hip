@@ -1,0 +1,274 @@
+// gated.hip -- the gated linear layer: h = f(x Wg^T) * (x Wu^T).
+//
+// Both projections are one product whose columns alternate between gate and up, 32 of each: a
+// wave then holds a token's g and u of the same channel in two accumulators, and the activation and the
+// product are the epilogue; neither projection goes to memory unless the backward pass wants it.
+#include "gated_core.hpp"
+
+namespace fp8dp {
+
+// Outputs of a wave's TM x TN tiles: columns n .. of the dual product are channels n / 2 ..
+template <typename T, int TM, int TN>
+struct GatedOut {
+  T *h, *gate, *up;
+  int M, N, act;
+  __device__ __forceinline__ void operator()(const v16f_t (&acc)[TM][TN], uint8_t* part, int m, int n,
+                                             int lane, int) const {
+    const int c0 = n / 2;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      auto emit = [&](T* to) {
+        return [=](int r, int c, const float v[8]) {
+          const int row = m + 32 * i + r, left = N - c0 - c;
+          if (row < M && left > 0) store8(to + (int64_t)row * N + c0 + c, left, v);
+        };
+      };
+      if (gate != nullptr) {
+        turn_tile<TN / 2>(part, lane, [&](int j, int r) { return acc[i][2 * j][r]; }, emit(gate));
+        turn_tile<TN / 2>(part, lane, [&](int j, int r) { return acc[i][2 * j + 1][r]; }, emit(up));
+      }
+      turn_tile<TN / 2>(
+          part, lane,
+          [&](int j, int r) { return gate_of<false>(act, acc[i][2 * j][r], nullptr) * acc[i][2 * j + 1][r]; },
+          emit(h));
+    }
+  }
+};
+
+// Sums of a range of K: parts[split][gate, up][M][N].
+template <int TM, int TN>
+struct GatedParts {
+  float* parts;
+  int M, N;
+  __device__ __forceinline__ void operator()(const v16f_t (&acc)[TM][TN], uint8_t* part, int m, int n,
+                                             int lane, int split) const {
+    const int c0 = n / 2;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        float* const to = parts + (int64_t)(2 * split + p) * M * N;
+        turn_tile<TN / 2>(
+            part, lane, [&](int j, int r) { return acc[i][2 * j + p][r]; },
+            [=](int r, int c, const float v[8]) {
+              const int row = m + 32 * i + r, left = N - c0 - c;
+              if (row < M && left > 0) store8(to + (int64_t)row * N + c0 + c, left, v);
+            });
+      }
+  }
+};
+
+// h (and g, u) from the sums of `splits` ranges.
+template <typename T>
+__global__ __launch_bounds__(256) void k_gated_join(const float* parts, int splits, int64_t total, T* h,
+                                                    T* gate, T* up, int act) {
+  const int64_t step = (int64_t)gridDim.x * 2048;
+  for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; at < total; at += step) {
+    const int n = (int)std::min<int64_t>(total - at, 8);
+    float g[8] = {}, u[8] = {};
+    for (int s = 0; s < splits; ++s) {
+      float a[8], b[8];
+      load8(parts + (2 * s) * total + at, n, a);
+      load8(parts + (2 * s + 1) * total + at, n, b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        g[j] += a[j];
+        u[j] += b[j];
+      }
+    }
+    if (gate != nullptr) {
+      store8(gate + at, n, g);
+      store8(up + at, n, u);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] = gate_of<false>(act, g[j], nullptr) * u[j];
+    store8(h + at, n, g);
+  }
+}
+
+// ------------------------------------------------------------------ few tokens
+// Up to 16 MT tokens: bound by the weights, which are read once.  A workgroup owns 16 channels; its waves take
+// the blocks of 128 k in turn and their sums are joined in LDS.  The matrix instruction 16 x 16 x 32 has the
+// weight's rows as its first operand, so a lane ends with one token and four channels.  Rows may start and
+// end at any byte: a chunk that K cuts is read as the row's last 8 values and shifted.
+constexpr int kFewWaves = 8, kFewTokens16 = 64;
+
+template <typename T>
+__device__ __forceinline__ v8s_t as_frag(const Raw8<T>& r) {
+  return __builtin_bit_cast(v8s_t, u32x4_t{r.w[0], r.w[1], r.w[2], r.w[3]});
+}
+
+template <typename T, int MT>
+__global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(const T* x, const T* w_gate, const T* w_up,
+                                                              int M, int N, int K, int act, T* h, T* gate,
+                                                              T* up) {
+  __shared__ v4f_t sums[kFewWaves][2][MT][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = blockIdx.x * 16, row = lane & 15, part = lane >> 4;
+  const int n = n0 + row < N ? n0 + row : N - 1;
+  const T *const wg = w_gate + (int64_t)n * K, *const wu = w_up + (int64_t)n * K;
+  const T* xr[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) xr[i] = x + (int64_t)(16 * i + row < M ? 16 * i + row : M - 1) * K;
+  v4f_t ag[MT], au[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) ag[i] = au[i] = v4f_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  auto block = [&](int k0, auto WHOLE) {
+    constexpr bool whole = decltype(WHOLE)::value;
+    Raw8<T> g[4], u[4], v[MT][4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int k = k0 + 32 * s + 8 * part;
+      auto load = [&](const T* p) {
+        if constexpr (whole) return load_raw8(p + k);
+        else return load_raw(p + k, K - k);
+      };
+      g[s] = load(wg);
+      u[s] = load(wu);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) v[i][s] = load(xr[i]);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        ag[i] = mma16(T{}, as_frag(g[s]), as_frag(v[i][s]), ag[i]);
+        au[i] = mma16(T{}, as_frag(u[s]), as_frag(v[i][s]), au[i]);
+      }
+  };
+  int k0 = wave * 128;
+  for (; k0 + 128 <= K; k0 += kFewWaves * 128) block(k0, std::true_type{});
+  if (k0 < K) block(k0, std::false_type{});
+
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    sums[wave][0][i][lane] = ag[i];
+    sums[wave][1][i][lane] = au[i];
+  }
+  __syncthreads();
+  if (wave >= MT) return;
+  v4f_t g = {0.0f, 0.0f, 0.0f, 0.0f}, u = g;
+#pragma unroll
+  for (int w = 0; w < kFewWaves; ++w) {
+    g += sums[w][0][wave][lane];
+    u += sums[w][1][wave][lane];
+  }
+  const int token = 16 * wave + row;
+  if (token >= M) return;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int c = n0 + 4 * part + r;
+    if (c >= N) continue;
+    const int64_t at = (int64_t)token * N + c;
+    h[at] = from_f32<T>(gate_of<false>(act, g[r], nullptr) * u[r]);
+    if (gate != nullptr) {
+      gate[at] = from_f32<T>(g[r]);
+      up[at] = from_f32<T>(u[r]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ launch
+static ProductPlan plan_gated(int64_t M, int64_t N, int64_t K, bool direct) {
+  return plan_product(M, 2 * N, (K + kStageK - 1) / kStageK, true, direct);
+}
+
+template <typename T, int WM, int WN, int TM, int TN, bool DIRECT>
+static int launch_gated(const char* what, MmaArgs g, int M, int N, int splits, int act, T* h, T* gate, T* up,
+                        float* parts, hipStream_t stream) {
+  g.tiles_m = (M + WM * TM * 32 - 1) / (WM * TM * 32);
+  g.tiles_n = (N + WN * TN * 16 - 1) / (WN * TN * 16);
+  return for_tiles((int64_t)g.tiles_m * g.tiles_n, [&](int first, unsigned count) {
+    g.first = first;
+    const dim3 grid(count, (unsigned)splits), block(64 * WM * WN);
+    if (splits > 1) {
+      const GatedParts<TM, TN> out = {parts, M, N};
+      hipLaunchKernelGGL((k_mma<T, WM, WN, TM, TN, false, false, true, DIRECT, GatedParts<TM, TN>>), grid,
+                         block, 0, stream, g, out);
+    } else {
+      const GatedOut<T, TM, TN> out = {h, gate, up, M, N, act};
+      hipLaunchKernelGGL((k_mma<T, WM, WN, TM, TN, false, false, true, DIRECT, GatedOut<T, TM, TN>>), grid,
+                         block, 0, stream, g, out);
+    }
+    return check_launch(what);
+  });
+}
+
+template <typename T>
+static int run_gated(const char* what, const T* x, const T* wg, const T* wu, int M, int N, int K, int act, T* h,
+                     T* gate, T* up, float* parts, int64_t parts_bytes, hipStream_t stream) {
+  if (M <= kFewTokens16) {
+    const dim3 grid((unsigned)((N + 15) / 16)), block(64 * kFewWaves);
+    auto few = [&](auto mt) {
+      hipLaunchKernelGGL((k_gated_few<T, decltype(mt)::value>), grid, block, 0, stream, x, wg, wu, M, N, K, act,
+                         h, gate, up);
+      return check_launch(what);
+    };
+    if (M <= 16) return few(std::integral_constant<int, 1>{});
+    if (M <= 32) return few(std::integral_constant<int, 2>{});
+    if (M <= 48) return few(std::integral_constant<int, 3>{});
+    return few(std::integral_constant<int, 4>{});
+  }
+  MmaArgs g = {};
+  g.a = {{reinterpret_cast<const uint16_t*>(x), reinterpret_cast<const uint16_t*>(x)}, K, M};
+  g.b = {{reinterpret_cast<const uint16_t*>(wg), reinterpret_cast<const uint16_t*>(wu)}, K, N};
+  g.stages = g.seg_stages = (K + kStageK - 1) / kStageK;
+  g.valid_a = g.valid_b = K;
+  const bool direct = rows16(g.a, K) && rows16(g.b, K);
+  ProductPlan p = plan_gated(M, N, K, direct);
+  if ((int64_t)p.splits * 2 * M * N * 4 > parts_bytes) p.splits = 1;
+  int rc;
+  if (p.shape == kTile256) rc = launch_gated<T, 4, 2, 2, 4, true>(what, g, M, N, p.splits, act, h, gate, up, parts, stream);
+  else if (direct) rc = launch_gated<T, 2, 2, 2, 2, true>(what, g, M, N, p.splits, act, h, gate, up, parts, stream);
+  else rc = launch_gated<T, 2, 2, 2, 2, false>(what, g, M, N, p.splits, act, h, gate, up, parts, stream);
+  if (rc || p.splits == 1) return rc;
+  const int64_t total = (int64_t)M * N;
+  hipLaunchKernelGGL((k_gated_join<T>), dim3(grid_for((total + 7) / 8, 256, 16)), dim3(256), 0, stream, parts,
+                     p.splits, total, h, gate, up, act);
+  return check_launch(what);
+}
+
+}  // namespace fp8dp
+
+using namespace fp8dp;
+
+extern "C" int64_t gated_linear_workspace(int64_t M, int64_t N, int64_t K) {
+  if (M <= kFewTokens16 || N < 1 || K < 1 || M > FP8DP_GATED_MAX_ROWS || N > FP8DP_GATED_MAX_WIDTH ||
+      K > FP8DP_GATED_MAX_WIDTH)
+    return 0;
+  const int splits = std::max(plan_gated(M, N, K, true).splits, plan_gated(M, N, K, false).splits);
+  return splits > 1 ? (int64_t)splits * 2 * M * N * 4 : 0;
+}
+
+extern "C" int gated_linear(const void* x, const void* w_gate, const void* w_up, int64_t M, int64_t N,
+                            int64_t K, fp8dp_dtype dt, fp8dp_gate act, void* h, void* gate, void* up,
+                            void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  const char* what = "gated_linear";
+  const int rc = check_gated(what, M, N, K, dt, act, workspace, workspace_bytes);
+  if (rc) return rc;
+  if (x == nullptr || w_gate == nullptr || w_up == nullptr || h == nullptr) {
+    set_error("%s: x, w_gate, w_up and h must be non-NULL", what);
+    return FP8DP_EINVAL;
+  }
+  if ((gate == nullptr) != (up == nullptr)) {
+    set_error("%s: gate and up go together", what);
+    return FP8DP_EINVAL;
+  }
+  if (!aligned_to(x, 2) || !aligned_to(w_gate, 2) || !aligned_to(w_up, 2) || !aligned_to(h, 2) ||
+      !aligned_to(gate, 2) || !aligned_to(up, 2))
+    return bad_align(what);
+  if (h == gate || h == up || (gate != nullptr && gate == up)) {
+    set_error("%s: h, gate and up must be different buffers", what);
+    return FP8DP_EINVAL;
+  }
+  auto run = [&](auto t) {
+    using T = decltype(t);
+    return run_gated<T>(what, static_cast<const T*>(x), static_cast<const T*>(w_gate),
+                        static_cast<const T*>(w_up), (int)M, (int)N, (int)K, act, static_cast<T*>(h),
+                        static_cast<T*>(gate), static_cast<T*>(up), static_cast<float*>(workspace),
+                        workspace == nullptr ? 0 : workspace_bytes, stream);
+  };
+  return dt == FP8DP_BF16 ? run(bf16_t{}) : run(f16_t{});
+}

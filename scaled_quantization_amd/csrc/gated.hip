@@ -7,30 +7,38 @@
 
 namespace fp8dp {
 
-// Outputs of a wave's TM x TN tiles: columns n .. of the dual product are channels n / 2 ..
+// Outputs of a wave's TM x TN tiles: columns n .. of the dual product are channels n / 2 ..  Of four column tiles
+// two are gate and two are up.
 template <typename T, int TM, int TN>
 struct GatedOut {
   T *h, *gate, *up;
   int M, N, act;
-  __device__ __forceinline__ void operator()(const v16f_t (&acc)[TM][TN], uint8_t* part, int m, int n,
+  __device__ __forceinline__ void operator()(const v4f_t (&acc)[TM][TN], uint8_t* part, int m, int n,
                                              int lane, int) const {
+    constexpr int JT = TN / 4;   // 32 channels each
     const int c0 = n / 2;
+    auto of = [](int j) { return j / 2 * 4 + j % 2; };   // gate's tile of channel tile j
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
+    for (int i0 = 0; i0 < TM; i0 += 2) {
       auto emit = [&](T* to) {
-        return [=](int r, int c, const float v[8]) {
-          const int row = m + 32 * i + r, left = N - c0 - c;
-          if (row < M && left > 0) store8(to + (int64_t)row * N + c0 + c, left, v);
+        return [=](int r, int c, const Raw8<T>& v) {
+          const int row = m + 16 * i0 + r, left = N - c0 - c;
+          if (row < M && left > 0) store_row(to + (int64_t)row * N + c0 + c, left, v);
         };
       };
+      with_act(act, [&](auto ACT) {
+        turn16<T, JT>(
+            part, lane,
+            [&](int i, int j, int r) {
+              return gate_of<decltype(ACT)::value, false>(acc[i0 + i][of(j)][r], nullptr) *
+                     acc[i0 + i][of(j) + 2][r];
+            },
+            emit(h));
+      });
       if (gate != nullptr) {
-        turn_tile<TN / 2>(part, lane, [&](int j, int r) { return acc[i][2 * j][r]; }, emit(gate));
-        turn_tile<TN / 2>(part, lane, [&](int j, int r) { return acc[i][2 * j + 1][r]; }, emit(up));
+        turn16<T, JT>(part, lane, [&](int i, int j, int r) { return acc[i0 + i][of(j)][r]; }, emit(gate));
+        turn16<T, JT>(part, lane, [&](int i, int j, int r) { return acc[i0 + i][of(j) + 2][r]; }, emit(up));
       }
-      turn_tile<TN / 2>(
-          part, lane,
-          [&](int j, int r) { return gate_of<false>(act, acc[i][2 * j][r], nullptr) * acc[i][2 * j + 1][r]; },
-          emit(h));
     }
   }
 };
@@ -40,19 +48,19 @@ template <int TM, int TN>
 struct GatedParts {
   float* parts;
   int M, N;
-  __device__ __forceinline__ void operator()(const v16f_t (&acc)[TM][TN], uint8_t* part, int m, int n,
+  __device__ __forceinline__ void operator()(const v4f_t (&acc)[TM][TN], uint8_t* part, int m, int n,
                                              int lane, int split) const {
     const int c0 = n / 2;
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int i0 = 0; i0 < TM; i0 += 2)
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        float* const to = parts + (int64_t)(2 * split + p) * M * N;
-        turn_tile<TN / 2>(
-            part, lane, [&](int j, int r) { return acc[i][2 * j + p][r]; },
-            [=](int r, int c, const float v[8]) {
-              const int row = m + 32 * i + r, left = N - c0 - c;
-              if (row < M && left > 0) store8(to + (int64_t)row * N + c0 + c, left, v);
+      for (int j0 = 0; j0 < TN; j0 += 2) {
+        float* const to = parts + (int64_t)(2 * split + j0 / 2 % 2) * M * N;
+        turn32(
+            part, lane, [&](int i, int j) { return acc[i0 + i][j0 + j]; },
+            [=](int r, int c, const Raw8<float>& v) {
+              const int row = m + 16 * i0 + r, col = c0 + j0 / 4 * 32 + c, left = N - col;
+              if (row < M && left > 0) store_row(to + (int64_t)row * N + col, left, v);
             });
       }
   }
@@ -80,8 +88,10 @@ __global__ __launch_bounds__(256) void k_gated_join(const float* parts, int spli
       store8(gate + at, n, g);
       store8(up + at, n, u);
     }
+    with_act(act, [&](auto ACT) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = gate_of<false>(act, g[j], nullptr) * u[j];
+      for (int j = 0; j < 8; ++j) g[j] = gate_of<decltype(ACT)::value, false>(g[j], nullptr) * u[j];
+    });
     store8(h + at, n, g);
   }
 }
@@ -157,12 +167,17 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(const T* x, const 
   }
   const int token = 16 * wave + row;
   if (token >= M) return;
+  float v[4];
+  with_act(act, [&](auto ACT) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = gate_of<decltype(ACT)::value, false>(g[r], nullptr) * u[r];
+  });
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int c = n0 + 4 * part + r;
     if (c >= N) continue;
     const int64_t at = (int64_t)token * N + c;
-    h[at] = from_f32<T>(gate_of<false>(act, g[r], nullptr) * u[r]);
+    h[at] = from_f32<T>(v[r]);
     if (gate != nullptr) {
       gate[at] = from_f32<T>(g[r]);
       up[at] = from_f32<T>(u[r]);
@@ -178,11 +193,12 @@ static ProductPlan plan_gated(int64_t M, int64_t N, int64_t K, bool direct) {
 template <typename T, int WM, int WN, int TM, int TN, bool DIRECT>
 static int launch_gated(const char* what, MmaArgs g, int M, int N, int splits, int act, T* h, T* gate, T* up,
                         float* parts, hipStream_t stream) {
-  g.tiles_m = (M + WM * TM * 32 - 1) / (WM * TM * 32);
-  g.tiles_n = (N + WN * TN * 16 - 1) / (WN * TN * 16);
-  return for_tiles((int64_t)g.tiles_m * g.tiles_n, [&](int first, unsigned count) {
+  g.tiles_m = (M + WM * TM * 16 - 1) / (WM * TM * 16);
+  g.tiles_n = (N + WN * TN * 8 - 1) / (WN * TN * 8);
+  g.splits = splits;
+  return for_work<DIRECT>((int64_t)g.tiles_m * g.tiles_n * splits, WM * WN == 8 ? 1 : 2, [&](int first, unsigned count) {
     g.first = first;
-    const dim3 grid(count, (unsigned)splits), block(64 * WM * WN);
+    const dim3 grid(count), block(64 * WM * WN);
     if (splits > 1) {
       const GatedParts<TM, TN> out = {parts, M, N};
       hipLaunchKernelGGL((k_mma<T, WM, WN, TM, TN, false, false, true, DIRECT, GatedParts<TM, TN>>), grid,
@@ -220,9 +236,9 @@ static int run_gated(const char* what, const T* x, const T* wg, const T* wu, int
   ProductPlan p = plan_gated(M, N, K, direct);
   if ((int64_t)p.splits * 2 * M * N * 4 > parts_bytes) p.splits = 1;
   int rc;
-  if (p.shape == kTile256) rc = launch_gated<T, 4, 2, 2, 4, true>(what, g, M, N, p.splits, act, h, gate, up, parts, stream);
-  else if (direct) rc = launch_gated<T, 2, 2, 2, 2, true>(what, g, M, N, p.splits, act, h, gate, up, parts, stream);
-  else rc = launch_gated<T, 2, 2, 2, 2, false>(what, g, M, N, p.splits, act, h, gate, up, parts, stream);
+  if (p.shape == kTile256) rc = launch_gated<T, 4, 2, 4, 8, true>(what, g, M, N, p.splits, act, h, gate, up, parts, stream);
+  else if (direct) rc = launch_gated<T, 2, 2, 4, 4, true>(what, g, M, N, p.splits, act, h, gate, up, parts, stream);
+  else rc = launch_gated<T, 2, 2, 4, 4, false>(what, g, M, N, p.splits, act, h, gate, up, parts, stream);
   if (rc || p.splits == 1) return rc;
   const int64_t total = (int64_t)M * N;
   hipLaunchKernelGGL((k_gated_join<T>), dim3(grid_for((total + 7) / 8, 256, 16)), dim3(256), 0, stream, parts,

@@ -27,13 +27,15 @@ __global__ __launch_bounds__(256) void k_gate_grad(const T* dh, const T* gate, c
     widen8f(rd, vd);
     widen8f(rg, g);
     widen8f(ru, u);
+    with_act(act, [&](auto ACT) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float slope;
-      const float f = gate_of<true>(act, g[j], &slope);
-      g[j] = vd[j] * u[j] * slope;
-      u[j] = vd[j] * f;
-    }
+      for (int j = 0; j < 8; ++j) {
+        float slope;
+        const float f = gate_of<decltype(ACT)::value, true>(g[j], &slope);
+        g[j] = vd[j] * u[j] * slope;
+        u[j] = vd[j] * f;
+      }
+    });
     T* const to = d + (int64_t)row * 2 * Np + c;
     const Raw8<T> dg = round8(g, T{}), du = round8(u, T{});
     *reinterpret_cast<u32x4_t*>(to) = u32x4_t{dg.w[0], dg.w[1], dg.w[2], dg.w[3]};
@@ -58,17 +60,20 @@ struct Rows2 {
 template <typename T, int TM, int TN>
 struct PlainOut {
   Rows2<T> rows;
-  __device__ __forceinline__ void operator()(const v16f_t (&acc)[TM][TN], uint8_t* part, int m, int n,
+  __device__ __forceinline__ void operator()(const v4f_t (&acc)[TM][TN], uint8_t* part, int m, int n,
                                              int lane, int) const {
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
-      turn_tile<TN>(
-          part, lane, [&](int j, int r) { return acc[i][j][r]; },
-          [&](int r, int c, const float v[8]) {
-            T* const y = rows.at(m + 32 * i + r);
-            const int left = rows.N - n - c;
-            if (y != nullptr && left > 0) store8(y + n + c, left, v);
-          });
+    for (int i0 = 0; i0 < TM; i0 += 2)
+      static_for<(TN + 3) / 4>([&](auto P) {
+        constexpr int j0 = 4 * decltype(P)::value;
+        turn16<T, (TN - j0 > 2 ? 2 : 1)>(
+            part, lane, [&](int i, int j, int r) { return acc[i0 + i][j0 + j][r]; },
+            [&](int r, int c, const Raw8<T>& v) {
+              T* const y = rows.at(m + 16 * i0 + r);
+              const int col = n + 16 * j0 + c, left = rows.N - col;
+              if (y != nullptr && left > 0) store_row(y + col, left, v);
+            });
+      });
   }
 };
 
@@ -77,17 +82,19 @@ template <int TM, int TN>
 struct PlainParts {
   float* parts;
   int M, N;
-  __device__ __forceinline__ void operator()(const v16f_t (&acc)[TM][TN], uint8_t* part, int m, int n,
+  __device__ __forceinline__ void operator()(const v4f_t (&acc)[TM][TN], uint8_t* part, int m, int n,
                                              int lane, int split) const {
     float* const to = parts + (int64_t)split * M * N;
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
-      turn_tile<TN>(
-          part, lane, [&](int j, int r) { return acc[i][j][r]; },
-          [&](int r, int c, const float v[8]) {
-            const int row = m + 32 * i + r, left = N - n - c;
-            if (row < M && left > 0) store8(to + (int64_t)row * N + n + c, left, v);
-          });
+    for (int i0 = 0; i0 < TM; i0 += 2)
+#pragma unroll
+      for (int j0 = 0; j0 < TN; j0 += 2)
+        turn32(
+            part, lane, [&](int i, int j) { return acc[i0 + i][j0 + j]; },
+            [&](int r, int c, const Raw8<float>& v) {
+              const int row = m + 16 * i0 + r, col = n + 16 * j0 + c, left = N - col;
+              if (row < M && left > 0) store_row(to + (int64_t)row * N + col, left, v);
+            });
   }
 };
 
@@ -114,11 +121,12 @@ __global__ __launch_bounds__(256) void k_plain_join(const float* parts, int spli
 template <typename T, int WM, int WN, int TM, int TN, bool ADOWN, bool DIRECT>
 static int launch_plain(const char* what, MmaArgs g, int m, int splits, Rows2<T> rows, float* parts,
                         hipStream_t stream) {
-  g.tiles_m = (m + WM * TM * 32 - 1) / (WM * TM * 32);
-  g.tiles_n = (rows.N + WN * TN * 32 - 1) / (WN * TN * 32);
-  return for_tiles((int64_t)g.tiles_m * g.tiles_n, [&](int first, unsigned count) {
+  g.tiles_m = (m + WM * TM * 16 - 1) / (WM * TM * 16);
+  g.tiles_n = (rows.N + WN * TN * 16 - 1) / (WN * TN * 16);
+  g.splits = splits;
+  return for_work<DIRECT>((int64_t)g.tiles_m * g.tiles_n * splits, WM * WN == 8 ? 1 : 2, [&](int first, unsigned count) {
     g.first = first;
-    const dim3 grid(count, (unsigned)splits), block(64 * WM * WN);
+    const dim3 grid(count), block(64 * WM * WN);
     if (splits > 1) {
       const PlainParts<TM, TN> out = {parts, m, rows.N};
       hipLaunchKernelGGL((k_mma<T, WM, WN, TM, TN, ADOWN, true, false, DIRECT, PlainParts<TM, TN>>), grid,
@@ -137,10 +145,10 @@ template <typename T, bool ADOWN>
 static int run_product(const char* what, const MmaArgs& g, int m, const ProductPlan& p, Rows2<T> rows,
                        float* parts, hipStream_t stream) {
   int rc;
-  if (p.shape == kTile256) rc = launch_plain<T, 4, 2, 2, 4, ADOWN, true>(what, g, m, p.splits, rows, parts, stream);
-  else if (p.shape == kTile192) rc = launch_plain<T, 4, 2, 2, 3, ADOWN, true>(what, g, m, p.splits, rows, parts, stream);
-  else if (p.shape == kTile128) rc = launch_plain<T, 2, 2, 2, 2, ADOWN, true>(what, g, m, p.splits, rows, parts, stream);
-  else rc = launch_plain<T, 2, 2, 2, 2, ADOWN, false>(what, g, m, p.splits, rows, parts, stream);
+  if (p.shape == kTile256) rc = launch_plain<T, 4, 2, 4, 8, ADOWN, true>(what, g, m, p.splits, rows, parts, stream);
+  else if (p.shape == kTile192) rc = launch_plain<T, 4, 2, 4, 6, ADOWN, true>(what, g, m, p.splits, rows, parts, stream);
+  else if (p.shape == kTile128) rc = launch_plain<T, 2, 2, 4, 4, ADOWN, true>(what, g, m, p.splits, rows, parts, stream);
+  else rc = launch_plain<T, 2, 2, 4, 4, ADOWN, false>(what, g, m, p.splits, rows, parts, stream);
   if (rc || p.splits == 1) return rc;
   const int64_t nvec = ((int64_t)rows.N + 7) / 8;
   hipLaunchKernelGGL((k_plain_join<T>), dim3(grid_for(m * nvec, 256, 16)), dim3(256), 0, stream, parts, p.splits,

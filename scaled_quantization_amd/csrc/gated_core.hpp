@@ -11,9 +11,9 @@ __device__ __forceinline__ float sigmoid_of(float g) {
 }
 // f(g), and f'(g) where GRAD.  The tails are formed without cancelling: sigmoid(v) for (1 + tanh(v / 2)) / 2
 // and the complementary error function for 1 + erf.
-template <bool GRAD>
-__device__ __forceinline__ float gate_of(int act, float g, float* slope) {
-  switch (act) {
+template <int ACT, bool GRAD>
+__device__ __forceinline__ float gate_of(float g, float* slope) {
+  switch (ACT) {
     case FP8DP_GATE_SILU: {
       const float p = sigmoid_of(g);
       if (GRAD) *slope = __builtin_fmaf(g * p, 1.0f - p, p);
@@ -49,6 +49,21 @@ __device__ __forceinline__ float gate_of(int act, float g, float* slope) {
     default:
       if (GRAD) *slope = 1.0f;
       return g;
+  }
+}
+
+// f(std::integral_constant<int, act>): one branch for a whole tile or kernel.  (A branch per element made 64 times seven
+// pieces of code of a tile's outputs, which the instruction cache does not hold: 7 us per tile of 256 x 256.)
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  switch (act) {
+    case FP8DP_GATE_SILU: return f(std::integral_constant<int, FP8DP_GATE_SILU>{});
+    case FP8DP_GATE_GELU: return f(std::integral_constant<int, FP8DP_GATE_GELU>{});
+    case FP8DP_GATE_GELU_TANH: return f(std::integral_constant<int, FP8DP_GATE_GELU_TANH>{});
+    case FP8DP_GATE_SIGMOID: return f(std::integral_constant<int, FP8DP_GATE_SIGMOID>{});
+    case FP8DP_GATE_RELU: return f(std::integral_constant<int, FP8DP_GATE_RELU>{});
+    case FP8DP_GATE_RELU2: return f(std::integral_constant<int, FP8DP_GATE_RELU2>{});
+    default: return f(std::integral_constant<int, FP8DP_GATE_IDENTITY>{});
   }
 }
 

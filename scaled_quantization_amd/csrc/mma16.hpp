@@ -26,14 +26,8 @@ typedef short v4s_t __attribute__((ext_vector_type(4)));
 typedef short v8s_t __attribute__((ext_vector_type(8)));
 typedef float v4f_t __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ v16f_t mma32(bf16_t, v8s_t a, v8s_t b, v16f_t c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf16_t, a),
-                                                 __builtin_bit_cast(v8bf16_t, b), c, 0, 0, 0);
-}
-__device__ __forceinline__ v16f_t mma32(f16_t, v8s_t a, v8s_t b, v16f_t c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8f16_t, a),
-                                                __builtin_bit_cast(v8f16_t, b), c, 0, 0, 0);
-}
+// The 16 x 16 x 32 instruction: its accumulators are read and written once per 32 k, those of 32 x 32 x 16 once per
+// 16, and the matrix pipes are bound by power: bare loops of them on normal data reach 2.06 and 1.83 PFLOP/s.
 __device__ __forceinline__ v4f_t mma16(bf16_t, v8s_t a, v8s_t b, v4f_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf16_t, a),
                                                  __builtin_bit_cast(v8bf16_t, b), c, 0, 0, 0);
@@ -44,6 +38,13 @@ __device__ __forceinline__ v4f_t mma16(f16_t, v8s_t a, v8s_t b, v4f_t c) {
 }
 
 constexpr int kStageK = 64;   // values of K per stage
+
+// The value, of which the compiler knows nothing: what is computed from it is not moved out of a loop, where it would
+// take registers from the products.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
 
 // What chunks past an operand's end are copied from.
 __device__ const u32x4_t kZeroChunk16 = {0, 0, 0, 0};
@@ -69,99 +70,148 @@ struct MmaArgs {
   int seg_stages;        // stages per piece of K (all of them where K is in one piece)
   int valid_a, valid_b;  // k of a piece that count, the others are zeros
   int stages;            // of all pieces
-  int tiles_m, tiles_n;
-  int first = 0;         // tile of workgroup 0
+  int tiles_m, tiles_n, splits;
+  int first = 0;         // piece of work of workgroup 0
 };
 
 // Byte of 16-byte chunk c of row k of a tile that lies down, R rows of the output's dimension wide.
 template <int R>
 __device__ __forceinline__ int down_swizzle(int k) {
-  return R % 128 == 0 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
+  return (R % 128 == 0 ? (k & 3) << 2 : ((k >> 1) & 1) << 2) | ((k >> 3) & 1) << 1;
 }
 template <int R>
 __device__ __forceinline__ int down_at(int k, int c) {
   return k * (R * 2) + ((c ^ down_swizzle<R>(k)) << 4);
 }
 
-// Moves tiles of R x 64 values into LDS with W waves.  DIRECT: rows start at multiples of 16 bytes
-// and are whole chunks, copied without passing registers; else through registers at any alignment.
+// Where a wave's copies of a tile's stage come from: the tile's first row of each piece (down: k = 0) and the
+// bytes to the next k, held in scalar registers.  (Read from the arguments by the piece's number they came as scalar
+// loads in the loop, each of which waited for all LDS reads under way.)
+template <int W, bool DOWN, bool DUAL>
+struct Source {
+  const uint8_t* base;
+  int64_t second, per_k;   // bytes from the first piece to the second, and to the next k
+  int wave;
+  __device__ __forceinline__ void init(const Operand& o, int r0, int wave_) {
+    wave = wave_;
+    const int64_t skip = DOWN ? 0 : (int64_t)(DUAL ? r0 / 2 : r0) * o.ld * 2;
+    base = reinterpret_cast<const uint8_t*>(o.p[0]) + skip;
+    second = reinterpret_cast<const uint8_t*>(o.p[1]) - reinterpret_cast<const uint8_t*>(o.p[0]);
+    per_k = DOWN ? o.ld * 2 : 2;
+  }
+  // Copy i's base at k of a piece.  DUAL: a copy's 8 rows are all of one piece.
+  __device__ __forceinline__ const uint8_t* at(int i, int piece, int k, int64_t more = 0) const {
+    const int64_t which = DUAL ? ((wave + W * i) >> 2) & 1 : piece;
+    return base + ((-which & second) + k * per_k + more);
+  }
+};
+
+// Moves tiles of R x 64 values into LDS with W waves, L copies of 1 KiB a wave and stage.
+// DIRECT: rows start at multiples of 16 bytes and are whole chunks, copied without passing registers.  Along, copy i's
+// rows are a fixed step behind copy 0's, and rows past the end are read as the last one; down, columns past the end are
+// read as the last chunk.  Neither is stored.
 template <typename T, int R, int W, bool DOWN, bool DUAL, bool DIRECT>
 struct Loader {
-  static constexpr int SIZE = R * 128;             // bytes of a tile
-  static constexpr int L = SIZE / 1024 / W;        // copies of a wave per stage
-  static_assert(SIZE % (1024 * W) == 0 && !(DUAL && DOWN), "whole copies");
-  uint32_t off[L];                                 // bytes from the stage's base
-  Raw8<T> reg[DIRECT ? 1 : L];
-  int cut[DIRECT ? 1 : L];                         // elements of the chunk inside the row (down)
-  int wave, lane;
+  static constexpr int SIZE = R * 128, L = SIZE / 1024 / W, CH = R / 8;
+  static constexpr bool EVEN = !DOWN || 64 * W % CH == 0;   // copies a fixed step apart
+  static_assert(DIRECT && SIZE % (1024 * W) == 0 && W % 2 == 0 && !(DUAL && DOWN), "whole copies");
+  Source<W, DOWN, DUAL> source;
+  uint32_t off[EVEN ? 1 : L], chunk;   // along: of copy 0's row, and of its chunk
+  uint32_t step, last;                 // along: between copies, and of the last row
+  int lane;
 
-  __device__ __forceinline__ void init(const Operand& o, int r0, int wave_, int lane_) {
-    wave = wave_;
+  __device__ __forceinline__ void init(const Operand& o, int r0, int wave, int lane_) {
+    source.init(o, r0, wave);
     lane = lane_;
+    const int l = opaque(lane_);
+    const uint32_t row = (uint32_t)(o.ld * 2);
+    if constexpr (DOWN) {
+#pragma unroll
+      for (int i = 0; i < (EVEN ? 1 : L); ++i) {
+        const int pos = (wave + W * i) * 64 + l, k = pos / CH;
+        const int m = r0 + ((pos % CH) ^ down_swizzle<R>(k)) * 8;
+        off[i] = (uint32_t)k * row + (uint32_t)(m > o.rows - 8 ? o.rows - 8 : m) * 2;
+      }
+    } else {
+      const int r = 8 * wave + (l >> 3);
+      off[0] = (uint32_t)(DUAL ? r & 31 : r) * row;
+      chunk = (uint32_t)((l & 7) ^ ((r >> 1) & 7)) * 16;
+      step = row;
+      last = (uint32_t)(o.rows - 1 - (DUAL ? r0 / 2 : r0)) * row;
+      if (o.rows - 1 - (DUAL ? r0 / 2 : r0) >= R) last = (uint32_t)R * row;   // (32 bits hold it)
+    }
+  }
+  // First k of copy i's chunk (along), or its row of k (down).
+  __device__ __forceinline__ int first_k(int i) const {
+    const int pos = (source.wave + W * i) * 64 + opaque(lane);
+    if constexpr (DOWN) return pos / CH;
+    else return ((pos % 8) ^ ((pos >> 4) & 7)) * 8;
+  }
+  // Copy I of the stage at k of a piece, of which `left` values of K count (64 or more: all).
+  template <int I>
+  __device__ __forceinline__ void copy_one(int piece, int k, int left, uint8_t* slot) {
+    uint32_t from;
+    int64_t more = 0;
+    if constexpr (DOWN) {
+      from = off[EVEN ? 0 : I];
+      if constexpr (EVEN) more = I * (64 * W / CH) * source.per_k;
+    } else {
+      // (opaque: kept once, not once for every copy)
+      const uint32_t r = (uint32_t)opaque((int)off[0]) + (DUAL ? 8 * W * I / 64 * 32 : 8 * W * I) * step;
+      from = (r < last ? r : last) + chunk;
+    }
+    const uint8_t* const b = source.at(I, piece, k, more);
+    uint8_t* const l = slot + (source.wave + W * I) * 1024;
+    if (left >= kStageK) {
+      copy16_to_lds_from(b, from, l);
+    } else {
+      copy16_to_lds(first_k(I) < left ? b + from : reinterpret_cast<const uint8_t*>(&kZeroChunk16), l);
+    }
+  }
+  __device__ __forceinline__ void copy(int piece, int k, int left, uint8_t* slot) {
+    static_for<L>([&](auto I) { copy_one<decltype(I)::value>(piece, k, left, slot); });
+  }
+};
+
+// The same through registers at any alignment: fetch starts the loads, put stores them to LDS.
+template <typename T, int R, int W, bool DOWN, bool DUAL>
+struct Loader<T, R, W, DOWN, DUAL, false> {
+  static constexpr int SIZE = R * 128, L = SIZE / 1024 / W, CH = R / 8;
+  static_assert(SIZE % (1024 * W) == 0 && !(DUAL && DOWN), "whole copies");
+  Source<W, DOWN, DUAL> source;
+  uint32_t off[L];   // bytes from the stage's base
+  int cut[L];        // down: elements of the chunk inside the row
+  Raw8<T> reg[L];
+  int lane;
+
+  __device__ __forceinline__ void init(const Operand& o, int r0, int wave, int lane_) {
+    source.init(o, r0, wave);
+    lane = lane_;
+    const uint32_t row = (uint32_t)(o.ld * 2);
 #pragma unroll
     for (int i = 0; i < L; ++i) {
-      const int pos = (wave + W * i) * 64 + lane;   // chunk of the tile in LDS
+      const int pos = (wave + W * i) * 64 + lane;
       if constexpr (DOWN) {
-        constexpr int CH = R / 8;
-        const int k = pos / CH, c = (pos % CH) ^ down_swizzle<R>(k);
-        int m = r0 + c * 8;
-        if constexpr (DIRECT) {
-          if (m > o.rows - 8) m = o.rows - 8;      // (columns past the end are not stored)
-        } else {
-          cut[i] = o.rows - m;
-          if (m > o.rows - 8) m = o.rows >= 8 ? o.rows - 8 : 0;
-        }
-        off[i] = (uint32_t)k * (uint32_t)(o.ld * 2) + (uint32_t)m * 2;
+        const int k = pos / CH, m = r0 + ((pos % CH) ^ down_swizzle<R>(k)) * 8, most = o.rows >= 8 ? o.rows - 8 : 0;
+        cut[i] = o.rows - m;
+        off[i] = (uint32_t)k * row + (uint32_t)(m > most ? most : m) * 2;
       } else {
-        const int r = pos / 8, c = (pos % 8) ^ ((r >> 1) & 7);
-        int m = DUAL ? r0 / 2 + (r >> 6) * 32 + (r & 31) : r0 + r;
-        if (m > o.rows - 1) m = o.rows - 1;        // (rows past the end are not stored)
-        // from the tile's first row, so that 32 bits hold it
-        off[i] = (uint32_t)(m - (DUAL ? r0 / 2 : r0)) * (uint32_t)(o.ld * 2) + (uint32_t)c * 16;
+        const int r = pos / 8, first = DUAL ? r0 / 2 : r0, c = (pos % 8) ^ ((r >> 1) & 7);
+        const int m = DUAL ? (r >> 6) * 32 + (r & 31) : r, most = o.rows - 1 - first;
+        off[i] = (uint32_t)(m > most ? most : m) * row + (uint32_t)c * 16;
       }
     }
   }
-  // the tile's first row, or for DOWN the first column
-  static __device__ __forceinline__ const uint8_t* base(const Operand& o, int piece, int r0, int k) {
-    const uint16_t* const p = piece ? o.p[1] : o.p[0];
-    if constexpr (DOWN) return reinterpret_cast<const uint8_t*>(p + (int64_t)k * o.ld);
-    else return reinterpret_cast<const uint8_t*>(p + (int64_t)(DUAL ? r0 / 2 : r0) * o.ld + k);
-  }
-  // First k of copy i's chunk (along), or its row of k (down).  For the last stage only: the lane is
-  // made opaque so that the result takes no registers in the loop.
   __device__ __forceinline__ int first_k(int i) const {
-    int l = lane;
-    asm volatile("" : "+v"(l));
-    const int pos = (wave + W * i) * 64 + l;
-    if constexpr (DOWN) return pos / (R / 8);
+    const int pos = (source.wave + W * i) * 64 + lane;
+    if constexpr (DOWN) return pos / CH;
     else return ((pos % 8) ^ ((pos >> 4) & 7)) * 8;
   }
-  // Which piece copy i's rows belong to (the same for its 8 rows, so for the wave).
-  __device__ __forceinline__ int dual_piece(int i) const { return ((wave + W * i) >> 2) & 1; }
-
-  // Stage at k of the piece, of which `left` values of K count (64 or more: all).
-  __device__ __forceinline__ void copy(const Operand& o, int piece, int r0, int k, int left, uint8_t* slot) {
-    static_for<L>([&](auto I) { copy_one<decltype(I)::value>(o, piece, r0, k, left, slot); });
-  }
-  template <int I>
-  __device__ __forceinline__ void copy_one(const Operand& o, int piece, int r0, int k, int left,
-                                           uint8_t* slot) {
-    static_assert(DIRECT, "");
-    const uint8_t* const b = base(o, DUAL ? dual_piece(I) : piece, r0, k);
-    uint8_t* const l = slot + (wave + W * I) * 1024;
-    if (left >= kStageK) {
-      copy16_to_lds_from(b, off[I], l);
-    } else {
-      copy16_to_lds(first_k(I) < left ? b + off[I] : reinterpret_cast<const uint8_t*>(&kZeroChunk16), l);
-    }
-  }
-  // The same through registers: fetch starts the loads, put stores them to LDS.
-  __device__ __forceinline__ void fetch(const Operand& o, int piece, int r0, int k, int left) {
+  __device__ __forceinline__ void fetch(const Operand& o, int piece, int k, int left) {
 #pragma unroll
     for (int i = 0; i < L; ++i) {
-      const uint8_t* const b = base(o, DUAL ? dual_piece(i) : piece, r0, k);
+      const T* const p = reinterpret_cast<const T*>(source.at(i, piece, k) + off[i]);
       if constexpr (DOWN) {
-        const T* const p = reinterpret_cast<const T*>(b + off[i]);
         if (first_k(i) >= left) {
           reg[i] = Raw8<T>{};
         } else if (o.rows >= 8) {
@@ -170,7 +220,7 @@ struct Loader {
           load_cut(p, o.rows, reg[i]);
         }
       } else {
-        reg[i] = load_raw(reinterpret_cast<const T*>(b + off[i]), left - first_k(i));
+        reg[i] = load_raw(p, left - first_k(i));
       }
     }
   }
@@ -180,67 +230,85 @@ struct Loader {
       if constexpr (DOWN) {
         if (o.rows >= 8) settle(reg[i], cut[i]);
       }
-      *reinterpret_cast<u32x4_t*>(slot + (wave + W * i) * 1024 + lane * 16) =
+      *reinterpret_cast<u32x4_t*>(slot + (source.wave + W * i) * 1024 + lane * 16) =
           u32x4_t{reg[i].w[0], reg[i].w[1], reg[i].w[2], reg[i].w[3]};
     }
   }
 };
 
-// Fragment of 32 rows (tile `ti` of 32) and 16 values of K (step q of 4) of a tile of R rows at `slot`:
-// lane l holds row l % 32 and k 8 (l / 32) .. + 7.
+// Fragment of 16 rows (tile `ti` of 16) and 32 values of K (half h of a stage) of a tile of R rows at `slot`:
+// lane l holds row l % 16 and k 8 (l / 16) .. + 7.
 template <int R, bool DOWN>
-__device__ __forceinline__ v8s_t fragment(const uint8_t* slot, int ti, int q, int lane) {
+__device__ __forceinline__ v8s_t fragment(const uint8_t* slot, int ti, int h, int lane) {
   if constexpr (DOWN) {
     typedef __attribute__((address_space(3))) v4s_t lds_v4s_t;
-    const int p = lane & 15;
-    const int k = 8 * (lane >> 5) + (p >> 2), c = 4 * ti + 2 * ((lane >> 4) & 1) + ((p & 3) >> 1);
-    const uint8_t* const at = slot + down_at<R>(k, c) + (p & 1) * 8 + q * 16 * R * 2;
+    const int p = lane & 15, k = 8 * (lane >> 4) + (p >> 2), c = 2 * ti + ((p & 3) >> 1);
+    const uint8_t* const at = slot + down_at<R>(k, c) + (p & 1) * 8 + h * 32 * R * 2;
     const v4s_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)at);
     const v4s_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)(at + 4 * R * 2));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   } else {
-    return *reinterpret_cast<const v8s_t*>(slot + swz(32 * ti + (lane & 31), 2 * q + (lane >> 5)));
+    return *reinterpret_cast<const v8s_t*>(slot + swz(16 * ti + (lane & 15), 4 * h + (lane >> 4)));
   }
 }
 
 // ------------------------------------------------------------------ the product
-// A workgroup of WM x WN waves owns BM x BN outputs, a wave TM x TN tiles of 32 x 32.  The product is
-// issued with B first, so a lane holds one m and register r the n 8 (r / 4) + 4 (lane / 32) + r % 4.
-// gridDim.y > 1: workgroup (t, s) takes the s-th range of stages.
-// out(acc, lds of the wave, m of the wave, n of the wave, split): stores the tile.
+// A workgroup of WM x WN waves owns BM x BN outputs, a wave 16 TM x 16 TN as tiles of 16 x 16.  The product is
+// issued with B first, so a lane holds m lane % 16 of a tile, and register r its n 4 (lane / 16) + r.
+// A piece of work is a tile and a range of K, of which there are `splits`.
+// out(acc, LDS of the wave, m of the wave, n of the wave, lane, split): stores the tile.
 //
 // DIRECT: two LDS slots filled by copies that pass no registers.  A stage goes in halves, with
 // fragments double-buffered: the first half of a stage is multiplied while its second is read, then one barrier
 // shows that all copies of the next stage have landed and that this slot has been read; the second
-// half is multiplied while the slot is refilled and the next stage's first half is read.
-// Else: loads of the next stage travel in registers while one is multiplied.
+// half is multiplied while the slot is refilled and the next stage's first half is read.  The copies are
+// spread over the half: the compute unit takes one in 16 cycles, and eight waves that issue theirs
+// at once wait for each other.
+// The grid is resident: a workgroup goes from one piece of work to the next in one pipeline, the last stages
+// of one refill the slots with the first of the next, so that its outputs are stored while they travel (outputs have
+// LDS of their own).  Stores count like copies where a wave waits for its copies: the ones under way before the outputs
+// are waited for ahead of the first store, and the first stage behind the outputs waits for none.
+// Else: loads of the next stage travel in registers while one is multiplied, a workgroup per piece of work.
+constexpr int kOutBytes = 4096;   // a wave's LDS for its outputs
+
+// Piece of work `i` of `n` in the order of workgroups b = i % grid: each XCD (workgroup b runs on XCD b % 8)
+// has consecutive ones in hand, of the last, cut pass too where that is a multiple of 8.
+__device__ __forceinline__ int work_of(int i, int n, int grid) {
+  const int pass = i / grid, b = i - pass * grid, left = n - pass * grid < grid ? n - pass * grid : grid;
+  return pass * grid + (left % 8 == 0 ? b % 8 * (left / 8) + b / 8 : b);
+}
+
 template <typename T, int WM, int WN, int TM, int TN, bool ADOWN, bool BDOWN, bool DUAL, bool DIRECT,
           typename Out>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_mma(MmaArgs g, Out out) {
-  constexpr int W = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
+  constexpr int W = WM * WN, BM = WM * TM * 16, BN = WN * TN * 16;
   using LoadA = Loader<T, BM, W, ADOWN, false, DIRECT>;
   using LoadB = Loader<T, BN, W, BDOWN, DUAL, DIRECT>;
   constexpr int SLOT = LoadA::SIZE + LoadB::SIZE, NCOPY = LoadA::L + LoadB::L;
-  constexpr int kTurn = 32 * 32 * TN * 4;   // bytes of a wave's part of LDS for the outputs
-  constexpr int LDS = 2 * SLOT > W * kTurn ? 2 * SLOT : W * kTurn;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[LDS];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * SLOT + W * kOutBytes];
 
-  const int ntiles = g.tiles_m * g.tiles_n;
-  const int tile = tile_of_block(g.first + (int)blockIdx.x, ntiles);
-  // bands 4 tiles wide: the 32 tiles that an XCD has in hand are 8 x 4, whose operands are 12 tiles
-  const int band = tile / (4 * g.tiles_m), in_band = tile - band * 4 * g.tiles_m;
-  const int wide = g.tiles_n - band * 4 < 4 ? g.tiles_n - band * 4 : 4;
-  const int m0 = in_band / wide * BM, n0 = (band * 4 + in_band % wide) * BN;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wr = wave / WN * TM, wc = wave % WN * TN;   // in tiles of 32
-  const int begin = (int)((int64_t)g.stages * blockIdx.y / gridDim.y);
-  const int end = (int)((int64_t)g.stages * (blockIdx.y + 1) / gridDim.y);
+  const int wr = wave / WN * TM, wc = wave % WN * TN;   // in tiles of 16
+  uint8_t* const part = lds + 2 * SLOT + wave * kOutBytes;
+  const int ntiles = g.tiles_m * g.tiles_n, total = ntiles * g.splits;
 
-  LoadA la;
-  LoadB lb;
-  la.init(g.a, m0, wave, lane);
-  lb.init(g.b, n0, wave, lane);
+  struct Work {
+    int m0, n0, begin, end, split;
+  };
+  auto work = [&](int i) -> Work {
+    const int w = work_of(i, total, DIRECT ? (int)gridDim.x : total);
+    const int split = w / ntiles, tile = w - split * ntiles;
+    // bands 4 tiles wide: the 32 tiles that an XCD has in hand are 8 x 4, whose operands are 12 tiles
+    const int band = tile / (4 * g.tiles_m), in_band = tile - band * 4 * g.tiles_m;
+    const int wide = g.tiles_n - band * 4 < 4 ? g.tiles_n - band * 4 : 4;
+    // (divisions leave their results in vector registers)
+    auto s = [](int v) { return (int)__builtin_amdgcn_readfirstlane(v); };
+    const int each = g.stages / g.splits, more = g.stages - each * g.splits;   // the first `more` ranges have one more
+    const int begin = split * each + (split < more ? split : more);
+    return {s(in_band / wide * BM), s((band * 4 + in_band % wide) * BN), s(begin),
+            s(begin + each + (split < more ? 1 : 0)), s(split)};
+  };
   struct At {
     int piece, k;
   };
@@ -249,116 +317,137 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mma(MmaArgs g, Out out) {
     return {piece, (kt - (piece ? g.seg_stages : 0)) * kStageK};
   };
 
-  v16f_t acc[TM][TN];
+  LoadA la;
+  LoadB lb;
+  v4f_t acc[TM][TN];
+  auto clear = [&]() {
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+      for (int j = 0; j < TN; ++j) acc[i][j] = v4f_t{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  clear();
 
   if constexpr (DIRECT) {
-    // fragments of two of a stage's four steps: one read of the 2 (TM + TN)
+    // fragments of half a stage: one read of the TM + TN
     struct Frags {
-      v8s_t a[2][TM], b[2][TN];
+      v8s_t a[TM], b[TN];
     };
     auto read_one = [&](auto X, const uint8_t* slot, int h, Frags& f) {
-      constexpr int x = decltype(X)::value, q = x / (TM + TN), i = x % (TM + TN);
-      if constexpr (i < TM) f.a[q][i] = fragment<BM, ADOWN>(slot, wr + i, 2 * h + q, lane);
-      else f.b[q][i - TM] = fragment<BN, BDOWN>(slot + LoadA::SIZE, wc + i - TM, 2 * h + q, lane);
+      constexpr int x = decltype(X)::value;
+      if constexpr (x < TM) f.a[x] = fragment<BM, ADOWN>(slot, wr + x, h, lane);
+      else f.b[x - TM] = fragment<BN, BDOWN>(slot + LoadA::SIZE, wc + x - TM, h, lane);
     };
-    constexpr int READS = 2 * (TM + TN), PRODUCTS = 2 * TM * TN;
-    constexpr int EACH = (READS + PRODUCTS - 1) / PRODUCTS, CEACH = (NCOPY + PRODUCTS - 1) / PRODUCTS;
+    constexpr int READS = TM + TN, PRODUCTS = TM * TN;
+    static_assert(READS <= PRODUCTS, "a read behind a product");
     // the products of a half stage, with between(0), between(1), ... after one each: reads and copies
     // issue while a product runs
     auto multiply = [&](const Frags& f, auto&& between) {
       static_for<PRODUCTS>([&](auto X) {
-        constexpr int x = decltype(X)::value, q = x / (TM * TN), i = x / TN % TM, j = x % TN;
-        acc[i][j] = mma32(T{}, f.b[q][j], f.a[q][i], acc[i][j]);
+        constexpr int x = decltype(X)::value, i = x / TN, j = x % TN;
+        acc[i][j] = mma16(T{}, f.b[j], f.a[i], acc[i][j]);
         between(X);
         __builtin_amdgcn_sched_barrier(0);
       });
     };
-    auto issue = [&](int kt) {
-      const At s = at(kt);
-      uint8_t* const slot = lds + ((kt - begin) & 1) * SLOT;
-      la.copy(g.a, s.piece, m0, s.k, g.valid_a - s.k, slot);
-      lb.copy(g.b, s.piece, n0, s.k, g.valid_b - s.k, slot + LoadA::SIZE);
+    // the stage to be copied next: to_kt of piece of work `to`, two stages ahead of the one that is multiplied
+    int to = blockIdx.x, to_kt = 0, to_end = 0;
+    auto issue = [&](uint8_t* slot, bool first) {
+      if (first || to_kt == to_end) {   // on to the next piece of work
+        if (!first) to += gridDim.x;
+        if (to >= total) return;
+        const Work w = work(to);
+        la.init(g.a, w.m0, wave, lane);
+        lb.init(g.b, w.n0, wave, lane);
+        to_kt = w.begin;
+        to_end = w.end;
+      }
+      const At s = at(to_kt++);
+      la.copy(s.piece, s.k, g.valid_a - s.k, slot);
+      lb.copy(s.piece, s.k, g.valid_b - s.k, slot + LoadA::SIZE);
     };
-    // the first stage from begin + 2 on that is not whole, or the end: the last one of a piece
-    const int least = g.valid_a < g.valid_b ? g.valid_a : g.valid_b;
-    int whole = end;
-    if (least < g.seg_stages * kStageK) {
-      const int last = begin + 2 < g.seg_stages ? g.seg_stages - 1 : g.stages - 1;
-      if (last < whole) whole = last;
-    }
-    if (begin < end) issue(begin);
-    if (begin + 1 < end) issue(begin + 1);
-    if (begin + 1 < end) wait_vmcnt<NCOPY>();
+#pragma unroll 1
+    for (int s = 0; s < 2; ++s) issue(lds + s * SLOT, s == 0);
+    if (to < total) wait_vmcnt<NCOPY>();
     else wait_vmcnt<0>();
     stage_barrier();
     Frags f0, f1;
-    if (begin < end) static_for<READS>([&](auto X) { read_one(X, lds, 0, f0); });
-    // one stage; COPY: the stage two later is whole and copied between the products (else ahead of
-    // them); NEXT: there is a next stage
-    auto stage = [&](int kt, auto COPY, auto NEXT) {
-      constexpr bool copy = decltype(COPY)::value, next = decltype(NEXT)::value;
-      uint8_t* const slot = lds + ((kt - begin) & 1) * SLOT;
-      const uint8_t* const after = lds + ((kt + 1 - begin) & 1) * SLOT;
+    uint32_t odd = 0;      // slot of the stage in hand
+    bool landed = false;   // its successor's copies have been waited for
+    // One stage.  COPY: the stage to be copied is whole and of the same piece of work, and copied between the
+    // products; else it is any, or none, and copied ahead of them.  The next stage's first half is read even where
+    // there is no next stage: nothing looks at it then.
+    auto stage = [&](int kt, auto COPY) {
+      constexpr bool copy = decltype(COPY)::value;
+      uint8_t* const slot = lds + odd * SLOT;
+      const uint8_t* const after = lds + (odd ^ 1) * SLOT;
+      odd ^= 1;
       auto reads = [&](auto X, const uint8_t* from, int h, Frags& f) {
-        static_for<EACH>([&](auto E) {
-          constexpr int x = decltype(X)::value * EACH + decltype(E)::value;
-          if constexpr (x < READS) read_one(std::integral_constant<int, x>{}, from, h, f);
-        });
+        if constexpr (decltype(X)::value < READS) read_one(X, from, h, f);
       };
       multiply(f0, [&](auto X) { reads(X, slot, 1, f1); });
       __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's reads of the stage are done
-      wait_vmcnt<0>();                      // its copies of the next one have landed
+      if (!landed) wait_vmcnt<0>();         // its copies of the next one have landed
+      landed = false;
       stage_barrier();
       const At s = at(kt + 2);
-      if constexpr (!copy) {
-        if (kt + 2 < end) issue(kt + 2);
-      }
+      if constexpr (!copy) issue(slot, false);
       multiply(f1, [&](auto X) {
-        if constexpr (next) reads(X, after, 0, f0);
+        reads(X, after, 0, f0);
         if constexpr (copy) {
-          static_for<CEACH>([&](auto E) {
-            constexpr int c = decltype(X)::value * CEACH + decltype(E)::value;
-            if constexpr (c < LoadA::L)
-              la.template copy_one<c>(g.a, s.piece, m0, s.k, kStageK, slot);
-            else if constexpr (c < NCOPY)
-              lb.template copy_one<c - LoadA::L>(g.b, s.piece, n0, s.k, kStageK, slot + LoadA::SIZE);
+          constexpr int x = decltype(X)::value, c0 = x * NCOPY / PRODUCTS, c1 = (x + 1) * NCOPY / PRODUCTS;
+          static_for<c1 - c0>([&](auto C) {
+            constexpr int c = c0 + decltype(C)::value;
+            if constexpr (c < LoadA::L) la.template copy_one<c>(s.piece, s.k, kStageK, slot);
+            else lb.template copy_one<c - LoadA::L>(s.piece, s.k, kStageK, slot + LoadA::SIZE);
           });
         }
       });
     };
-    using yes = std::true_type;
-    using no = std::false_type;
-    int kt = begin;
-    for (; kt < whole - 2; ++kt) stage(kt, yes{}, yes{});
-    for (; kt + 1 < end; ++kt) stage(kt, no{}, yes{});
-    if (kt < end) stage(kt, no{}, no{});
+    const int least = g.valid_a < g.valid_b ? g.valid_a : g.valid_b;
+    for (int i = blockIdx.x; i < total; i += gridDim.x) {
+      const Work now = work(i);
+      // (read again behind the outputs, which need their registers)
+      static_for<READS>([&](auto X) { read_one(X, lds + odd * SLOT, 0, f0); });
+      // the first stage from begin + 2 on that is not whole, or the end: the last one of a piece of K
+      int whole = now.end;
+      if (least < g.seg_stages * kStageK) {
+        const int last = now.begin + 2 < g.seg_stages ? g.seg_stages - 1 : g.stages - 1;
+        if (last < whole) whole = last;
+      }
+      int kt = now.begin;
+      if (kt < whole - 2) {
+        for (; kt < whole - 2; ++kt) stage(kt, std::true_type{});
+        to_kt = whole;
+      }
+      for (; kt < now.end; ++kt) stage(kt, std::false_type{});
+      wait_vmcnt<0>();
+      landed = true;
+      out(acc, part, now.m0 + wr * 16, now.n0 + wc * 16, opaque(lane), now.split);
+      clear();
+    }
   } else {
+    const Work now = work(g.first + blockIdx.x);
+    la.init(g.a, now.m0, wave, lane);
+    lb.init(g.b, now.n0, wave, lane);
     auto fetch = [&](int kt) {
       const At s = at(kt);
-      la.fetch(g.a, s.piece, m0, s.k, g.valid_a - s.k);
-      lb.fetch(g.b, s.piece, n0, s.k, g.valid_b - s.k);
+      la.fetch(g.a, s.piece, s.k, g.valid_a - s.k);
+      lb.fetch(g.b, s.piece, s.k, g.valid_b - s.k);
     };
     auto put = [&](int kt) {
-      uint8_t* const slot = lds + ((kt - begin) & 1) * SLOT;
+      uint8_t* const slot = lds + ((kt - now.begin) & 1) * SLOT;
       la.put(g.a, slot);
       lb.put(g.b, slot + LoadA::SIZE);
     };
-    if (begin < end) {
-      fetch(begin);
-      put(begin);
-    }
+    fetch(now.begin);
+    put(now.begin);
     __syncthreads();
-    for (int kt = begin; kt < end; ++kt) {
-      if (kt + 1 < end) fetch(kt + 1);
-      const uint8_t* const slot = lds + ((kt - begin) & 1) * SLOT;
+    for (int kt = now.begin; kt < now.end; ++kt) {
+      if (kt + 1 < now.end) fetch(kt + 1);
+      const uint8_t* const slot = lds + ((kt - now.begin) & 1) * SLOT;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < 2; ++q) {
         v8s_t fa[TM], fb[TN];
 #pragma unroll
         for (int i = 0; i < TM; ++i) fa[i] = fragment<BM, ADOWN>(slot, wr + i, q, lane);
@@ -367,51 +456,78 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mma(MmaArgs g, Out out) {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
-          for (int j = 0; j < TN; ++j) acc[i][j] = mma32(T{}, fb[j], fa[i], acc[i][j]);
+          for (int j = 0; j < TN; ++j) acc[i][j] = mma16(T{}, fb[j], fa[i], acc[i][j]);
       }
-      if (kt + 1 < end) put(kt + 1);
+      if (kt + 1 < now.end) put(kt + 1);
       __syncthreads();
     }
+    out(acc, part, now.m0 + wr * 16, now.n0 + wc * 16, lane, now.split);
   }
-  // (all waves have read their last fragments: of DIRECT after the last stage's barrier nothing is read)
-  out(acc, lds + wave * kTurn, m0 + wr * 32, n0 + wc * 32, lane, (int)blockIdx.y);
 }
 
-// Turns 32 rows x 32 JT columns of a wave through its part of LDS: value(j, r) is register r of column
-// tile j in the layout above; emit(row, column, v) gets 8 consecutive columns, so that rows are
-// stored in whole cache lines.  16-byte chunks are swizzled by row against bank conflicts.
-template <int JT, typename Value, typename Emit>
-__device__ __forceinline__ void turn_tile(uint8_t* part, int lane, Value&& value, Emit&& emit) {
-  constexpr int CW = JT * 32, LPR = CW / 8;   // columns, lanes per row
-  auto at = [&](int r, int c) {               // byte of chunk c (4 columns) of row r
-    return r * CW * 4 + ((c ^ (JT == 1 ? (r >> 1) & 7 : JT == 3 ? r & 7 : r & 15)) << 4);
+// Outputs of a wave, 32 rows (two tiles) at a time, turned through its LDS so that rows are stored in whole pieces of
+// 8 columns.  In 16 bits: 32 JT columns; value(i, j, r) is register r of row tile i (0, 1) and column tile j in
+// the layout above; emit(row, column, v) gets 8 consecutive columns, a row's from 4 JT lanes.  16-byte chunks are
+// swizzled by row against bank conflicts.
+template <typename T, int JT, typename Value, typename Emit>
+__device__ __forceinline__ void turn16(uint8_t* part, int lane, Value&& value, Emit&& emit) {
+  static_assert(JT == 1 || JT == 2, "");
+  constexpr int PITCH = JT * 64, LPR = JT * 4;   // bytes and lanes per row
+  auto at = [&](int r, int c) {                  // byte of chunk c (8 columns) of row r
+    return r * PITCH + ((c ^ (JT == 2 ? r & 7 : (r >> 1) & 3)) << 4);
   };
-  const int frow = lane & 31, fhalf = lane >> 5;
 #pragma unroll
-  for (int j = 0; j < JT; ++j)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      v4f_t v;
+    for (int j = 0; j < 2 * JT; ++j) {
+      float v[8] = {};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = value(j, 4 * q + r);
-      *reinterpret_cast<v4f_t*>(part + at(frow, j * 8 + 2 * q + fhalf)) = v;
+      for (int r = 0; r < 4; ++r) v[r] = value(i, j, r);
+      const Raw8<T> w = round8(v, T{});
+      *reinterpret_cast<uint2*>(part + at(16 * i + (lane & 15), 2 * j + (lane >> 5)) + ((lane >> 4) & 1) * 8) =
+          make_uint2(w.w[0], w.w[1]);
     }
 #pragma unroll
   for (int s = 0; s < LPR / 2; ++s) {
-    const int x = s * 64 + lane, r = x / LPR, c = x % LPR * 2;
+    const int x = s * 64 + lane, r = x / LPR, c = x % LPR;
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(part + at(r, c));
+    Raw8<T> w;
+    w.w = u32x4_e_t{v[0], v[1], v[2], v[3]};
+    emit(r, c * 8, w);
+  }
+}
+// In 32 bits: 32 columns, a row's from 4 lanes.
+template <typename Value, typename Emit>
+__device__ __forceinline__ void turn32(uint8_t* part, int lane, Value&& value, Emit&& emit) {
+  auto at = [&](int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); };   // chunk c: 4 columns
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      *reinterpret_cast<v4f_t*>(part + at(16 * i + (lane & 15), 4 * j + (lane >> 4))) = value(i, j);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int r = s * 16 + (lane >> 2), c = (lane & 3) * 2;
     const v4f_t lo = *reinterpret_cast<const v4f_t*>(part + at(r, c));
     const v4f_t hi = *reinterpret_cast<const v4f_t*>(part + at(r, c + 1));
-    const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    emit(r, c * 4, v);
+    Raw8<float> w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w.lo[j] = lo[j];
+      w.hi[j] = hi[j];
+    }
+    emit(r, c * 4, w);
   }
 }
 
-// A launch has at most 2^32 - 1 threads; launch(first, count) in parts of a multiple of 8 tiles.
-template <typename F>
-inline int for_tiles(int64_t tiles, F&& launch) {
+// Runs a product's pieces of work: a resident grid where DIRECT, else a workgroup each (in launches of at most 2^32 - 1
+// threads).
+template <bool DIRECT, typename F>
+inline int for_work(int64_t total, int per_cu, F&& launch) {
+  if (DIRECT) return launch(0, (unsigned)std::min<int64_t>(total, (int64_t)num_cus() * per_cu));
   constexpr int64_t kMost = (int64_t)1 << 22;
-  for (int64_t first = 0; first < tiles; first += kMost) {
-    const int rc = launch((int)first, (unsigned)std::min(tiles - first, kMost));
+  for (int64_t first = 0; first < total; first += kMost) {
+    const int rc = launch((int)first, (unsigned)std::min(total - first, kMost));
     if (rc) return rc;
   }
   return FP8DP_OK;

@@ -107,24 +107,26 @@ struct Source {
 };
 
 // Moves tiles of R x 64 values into LDS with W waves, L copies of 1 KiB a wave and stage.
-// DIRECT: rows start at multiples of 16 bytes and are whole chunks, copied without passing registers.  Along, copy i's
-// rows are a fixed step behind copy 0's, and rows past the end are read as the last one; down, columns past the end are
-// read as the last chunk.  Neither is stored.
+// DIRECT: rows start at multiples of 16 bytes and are whole chunks, copied without passing registers.  Along, rows past
+// the end are read as the last one; down, columns past the end are read as the last chunk.  Neither is stored.
 template <typename T, int R, int W, bool DOWN, bool DUAL, bool DIRECT>
 struct Loader {
   static constexpr int SIZE = R * 128, L = SIZE / 1024 / W, CH = R / 8;
-  static constexpr bool EVEN = !DOWN || 64 * W % CH == 0;   // copies a fixed step apart
-  static_assert(DIRECT && SIZE % (1024 * W) == 0 && W % 2 == 0 && !(DUAL && DOWN), "whole copies");
-  Source<W, DOWN, DUAL> source;
-  uint32_t off[EVEN ? 1 : L], chunk;   // along: of copy 0's row, and of its chunk
-  uint32_t step, last;                 // along: between copies, and of the last row
-  int lane;
+  static constexpr bool EVEN = DOWN && 64 * W % CH == 0;   // copies are a fixed number of whole rows of k apart
+  static_assert(DIRECT && SIZE % (1024 * W) == 0 && (W == 4 || W == 8) && !(DUAL && DOWN), "whole copies");
+  const uint8_t *base, *here;    // of the tile, and of the stage to be copied
+  int64_t second, per_k;         // bytes from the first piece to the second, and to the next k
+  uint32_t off[EVEN ? 1 : L];
+  int wave, lane;
 
-  __device__ __forceinline__ void init(const Operand& o, int r0, int wave, int lane_) {
-    source.init(o, r0, wave);
+  __device__ __forceinline__ void init(const Operand& o, int r0, int wave_, int lane_) {
+    wave = wave_;
     lane = lane_;
     const int l = opaque(lane_);
     const uint32_t row = (uint32_t)(o.ld * 2);
+    per_k = DOWN ? o.ld * 2 : 2;
+    base = reinterpret_cast<const uint8_t*>(o.p[0]);
+    second = reinterpret_cast<const uint8_t*>(o.p[1]) - base;
     if constexpr (DOWN) {
 #pragma unroll
       for (int i = 0; i < (EVEN ? 1 : L); ++i) {
@@ -133,43 +135,42 @@ struct Loader {
         off[i] = (uint32_t)k * row + (uint32_t)(m > o.rows - 8 ? o.rows - 8 : m) * 2;
       }
     } else {
-      const int r = 8 * wave + (l >> 3);
-      off[0] = (uint32_t)(DUAL ? r & 31 : r) * row;
-      chunk = (uint32_t)((l & 7) ^ ((r >> 1) & 7)) * 16;
-      step = row;
-      last = (uint32_t)(o.rows - 1 - (DUAL ? r0 / 2 : r0)) * row;
-      if (o.rows - 1 - (DUAL ? r0 / 2 : r0) >= R) last = (uint32_t)R * row;   // (32 bits hold it)
+      const int first = DUAL ? r0 / 2 : r0, most = o.rows - 1 - first;
+      base += (int64_t)first * o.ld * 2;
+      // a copy's 8 rows are all of one piece: of eight waves the upper four have the second's, of four the odd copies
+      if (DUAL && W == 8) base += (wave >> 2) * second;
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        const int pos = (wave + W * i) * 64 + l, r = pos / 8, m = DUAL ? (r >> 6) * 32 + (r & 31) : r;
+        off[i] = (uint32_t)(m > most ? most : m) * row + (uint32_t)((pos % 8) ^ ((r >> 1) & 7)) * 16;
+      }
     }
   }
+  // On to the stage at k of a piece, and to the one behind it.
+  __device__ __forceinline__ void go(int piece, int k) { here = base + (DUAL ? 0 : piece * second) + k * per_k; }
+  __device__ __forceinline__ void step() { here += kStageK * per_k; }
   // First k of copy i's chunk (along), or its row of k (down).
   __device__ __forceinline__ int first_k(int i) const {
-    const int pos = (source.wave + W * i) * 64 + opaque(lane);
+    const int pos = (wave + W * i) * 64 + opaque(lane);
     if constexpr (DOWN) return pos / CH;
     else return ((pos % 8) ^ ((pos >> 4) & 7)) * 8;
   }
-  // Copy I of the stage at k of a piece, of which `left` values of K count (64 or more: all).
+  // Copy I of the stage, of which `left` values of K count (64 or more: all).
   template <int I>
-  __device__ __forceinline__ void copy_one(int piece, int k, int left, uint8_t* slot) {
-    uint32_t from;
-    int64_t more = 0;
-    if constexpr (DOWN) {
-      from = off[EVEN ? 0 : I];
-      if constexpr (EVEN) more = I * (64 * W / CH) * source.per_k;
-    } else {
-      // (opaque: kept once, not once for every copy)
-      const uint32_t r = (uint32_t)opaque((int)off[0]) + (DUAL ? 8 * W * I / 64 * 32 : 8 * W * I) * step;
-      from = (r < last ? r : last) + chunk;
-    }
-    const uint8_t* const b = source.at(I, piece, k, more);
-    uint8_t* const l = slot + (source.wave + W * I) * 1024;
+  __device__ __forceinline__ void copy_one(int left, uint8_t* slot) {
+    const uint8_t* b = here;
+    if constexpr (DUAL && W == 4) b += I % 2 * second;
+    if constexpr (EVEN) b += I * (64 * W / CH) * per_k;
+    const uint32_t from = off[EVEN ? 0 : I];
+    uint8_t* const l = slot + (wave + W * I) * 1024;
     if (left >= kStageK) {
       copy16_to_lds_from(b, from, l);
     } else {
       copy16_to_lds(first_k(I) < left ? b + from : reinterpret_cast<const uint8_t*>(&kZeroChunk16), l);
     }
   }
-  __device__ __forceinline__ void copy(int piece, int k, int left, uint8_t* slot) {
-    static_for<L>([&](auto I) { copy_one<decltype(I)::value>(piece, k, left, slot); });
+  __device__ __forceinline__ void copy(int left, uint8_t* slot) {
+    static_for<L>([&](auto I) { copy_one<decltype(I)::value>(left, slot); });
   }
 };
 
@@ -236,21 +237,37 @@ struct Loader<T, R, W, DOWN, DUAL, false> {
   }
 };
 
-// Fragment of 16 rows (tile `ti` of 16) and 32 values of K (half h of a stage) of a tile of R rows at `slot`:
-// lane l holds row l % 16 and k 8 (l / 16) .. + 7.
+// Fragments of 16 rows and 32 values of K (half h of a stage): lane l holds row l % 16 and k 8 (l / 16) .. + 7.
+// start() is the LDS address of a wave's first tile (of 16 rows, tile t0 of the workgroup's R / 16) in the tile at `slot`;
+// read() that of its j-th.  The offsets are constants, or one exclusive-or away.
+typedef __attribute__((address_space(3))) v4s_t lds_v4s_t;
+typedef __attribute__((address_space(3))) v8s_t lds_v8s_t;
 template <int R, bool DOWN>
-__device__ __forceinline__ v8s_t fragment(const uint8_t* slot, int ti, int h, int lane) {
-  if constexpr (DOWN) {
-    typedef __attribute__((address_space(3))) v4s_t lds_v4s_t;
-    const int p = lane & 15, k = 8 * (lane >> 4) + (p >> 2), c = 2 * ti + ((p & 3) >> 1);
-    const uint8_t* const at = slot + down_at<R>(k, c) + (p & 1) * 8 + h * 32 * R * 2;
-    const v4s_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)at);
-    const v4s_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)(at + 4 * R * 2));
-    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-  } else {
-    return *reinterpret_cast<const v8s_t*>(slot + swz(16 * ti + (lane & 15), 4 * h + (lane >> 4)));
+struct Fragments {
+  static __device__ __forceinline__ uint32_t start(const uint8_t* slot, int t0, int h, int lane) {
+    const uint32_t at = (uint32_t)(uintptr_t)(lds_void_t*)slot;
+    if constexpr (DOWN) {
+      const int p = lane & 15, k = 8 * (lane >> 4) + (p >> 2);
+      const uint32_t lead = at + (h * 32 + k) * (R * 2) + (down_swizzle<R>(k) << 4) + ((p & 3) >> 1) * 16 + (p & 1) * 8;
+      return R % 128 == 0 ? lead ^ (uint32_t)(t0 << 5) : lead;
+    } else {
+      return at + swz(16 * t0 + (lane & 15), 4 * h + (lane >> 4));
+    }
   }
-}
+  static __device__ __forceinline__ v8s_t read(uint32_t start, int t0, int j) {
+    if constexpr (DOWN) {
+      // (a slot is a multiple of a row of k and of 512 bytes; rows of 192 values are not: there the swizzle stays within 128)
+      uint32_t at;
+      if constexpr (R % 128 == 0) at = start ^ (uint32_t)(j << 5);
+      else at = (start ^ (uint32_t)(((t0 + j) & 3) << 5)) + (uint32_t)((t0 + j) >> 2) * 128;
+      const v4s_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)(uintptr_t)at);
+      const v4s_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)(uintptr_t)(at + 4 * R * 2));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      return *(const lds_v8s_t*)(uintptr_t)(start + j * 2048);
+    }
+  }
+};
 
 // ------------------------------------------------------------------ the product
 // A workgroup of WM x WN waves owns BM x BN outputs, a wave 16 TM x 16 TN as tiles of 16 x 16.  The product is
@@ -285,7 +302,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mma(MmaArgs g, Out out) {
   using LoadA = Loader<T, BM, W, ADOWN, false, DIRECT>;
   using LoadB = Loader<T, BN, W, BDOWN, DUAL, DIRECT>;
   constexpr int SLOT = LoadA::SIZE + LoadB::SIZE, NCOPY = LoadA::L + LoadB::L;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * SLOT + W * kOutBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * SLOT + W * kOutBytes];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -330,13 +347,18 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mma(MmaArgs g, Out out) {
 
   if constexpr (DIRECT) {
     // fragments of half a stage: one read of the TM + TN
+    using FragA = Fragments<BM, ADOWN>;
+    using FragB = Fragments<BN, BDOWN>;
     struct Frags {
       v8s_t a[TM], b[TN];
     };
-    auto read_one = [&](auto X, const uint8_t* slot, int h, Frags& f) {
+    // addresses of the second halves in the slot in hand, and of the first halves in the other one
+    uint32_t a1 = FragA::start(lds, wr, 1, lane), b1 = FragB::start(lds + LoadA::SIZE, wc, 1, lane);
+    uint32_t a0 = FragA::start(lds + SLOT, wr, 0, lane), b0 = FragB::start(lds + SLOT + LoadA::SIZE, wc, 0, lane);
+    auto read_one = [&](auto X, uint32_t a, uint32_t b, Frags& f) {
       constexpr int x = decltype(X)::value;
-      if constexpr (x < TM) f.a[x] = fragment<BM, ADOWN>(slot, wr + x, h, lane);
-      else f.b[x - TM] = fragment<BN, BDOWN>(slot + LoadA::SIZE, wc + x - TM, h, lane);
+      if constexpr (x < TM) f.a[x] = FragA::read(a, wr, x);
+      else f.b[x - TM] = FragB::read(b, wc, x - TM);
     };
     constexpr int READS = TM + TN, PRODUCTS = TM * TN;
     static_assert(READS <= PRODUCTS, "a read behind a product");
@@ -363,8 +385,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mma(MmaArgs g, Out out) {
         to_end = w.end;
       }
       const At s = at(to_kt++);
-      la.copy(s.piece, s.k, g.valid_a - s.k, slot);
-      lb.copy(s.piece, s.k, g.valid_b - s.k, slot + LoadA::SIZE);
+      la.go(s.piece, s.k);
+      lb.go(s.piece, s.k);
+      la.copy(g.valid_a - s.k, slot);
+      lb.copy(g.valid_b - s.k, slot + LoadA::SIZE);
     };
 #pragma unroll 1
     for (int s = 0; s < 2; ++s) issue(lds + s * SLOT, s == 0);
@@ -372,55 +396,65 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mma(MmaArgs g, Out out) {
     else wait_vmcnt<0>();
     stage_barrier();
     Frags f0, f1;
-    uint32_t odd = 0;      // slot of the stage in hand
-    bool landed = false;   // its successor's copies have been waited for
-    // One stage.  COPY: the stage to be copied is whole and of the same piece of work, and copied between the
+    uint32_t hand = 0;     // the slot of the stage in hand, in bytes
+    bool landed = false;   // the copies of the stage behind it have been waited for
+    // One stage.  COPY: the stage to be copied is whole and the one behind the last copied, and copied between the
     // products; else it is any, or none, and copied ahead of them.  The next stage's first half is read even where
     // there is no next stage: nothing looks at it then.
-    auto stage = [&](int kt, auto COPY) {
+    auto stage = [&](auto COPY) {
       constexpr bool copy = decltype(COPY)::value;
-      uint8_t* const slot = lds + odd * SLOT;
-      const uint8_t* const after = lds + (odd ^ 1) * SLOT;
-      odd ^= 1;
-      auto reads = [&](auto X, const uint8_t* from, int h, Frags& f) {
-        if constexpr (decltype(X)::value < READS) read_one(X, from, h, f);
-      };
-      multiply(f0, [&](auto X) { reads(X, slot, 1, f1); });
+      uint8_t* const slot = lds + hand;
+      multiply(f0, [&](auto X) {
+        if constexpr (decltype(X)::value < READS) read_one(X, a1, b1, f1);
+      });
       __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's reads of the stage are done
       if (!landed) wait_vmcnt<0>();         // its copies of the next one have landed
       landed = false;
       stage_barrier();
-      const At s = at(kt + 2);
       if constexpr (!copy) issue(slot, false);
       multiply(f1, [&](auto X) {
-        reads(X, after, 0, f0);
+        constexpr int x = decltype(X)::value, c0 = x * NCOPY / PRODUCTS, c1 = (x + 1) * NCOPY / PRODUCTS;
+        if constexpr (x < READS) read_one(X, a0, b0, f0);
         if constexpr (copy) {
-          constexpr int x = decltype(X)::value, c0 = x * NCOPY / PRODUCTS, c1 = (x + 1) * NCOPY / PRODUCTS;
           static_for<c1 - c0>([&](auto C) {
             constexpr int c = c0 + decltype(C)::value;
-            if constexpr (c < LoadA::L) la.template copy_one<c>(s.piece, s.k, kStageK, slot);
-            else lb.template copy_one<c - LoadA::L>(s.piece, s.k, kStageK, slot + LoadA::SIZE);
+            if constexpr (c < LoadA::L) la.template copy_one<c>(kStageK, slot);
+            else lb.template copy_one<c - LoadA::L>(kStageK, slot + LoadA::SIZE);
           });
         }
       });
+      if constexpr (copy) {
+        la.step();
+        lb.step();
+      }
+      const uint32_t over = SLOT - 2 * hand;   // to the other slot
+      a1 += over;
+      b1 += over;
+      a0 -= over;
+      b0 -= over;
+      hand += over;
     };
     const int least = g.valid_a < g.valid_b ? g.valid_a : g.valid_b;
+    const int cut = least < g.seg_stages * kStageK ? 1 : 0;   // the last stage of a piece of K is not whole
     for (int i = blockIdx.x; i < total; i += gridDim.x) {
       const Work now = work(i);
-      // (read again behind the outputs, which need their registers)
-      static_for<READS>([&](auto X) { read_one(X, lds + odd * SLOT, 0, f0); });
-      // the first stage from begin + 2 on that is not whole, or the end: the last one of a piece of K
-      int whole = now.end;
-      if (least < g.seg_stages * kStageK) {
-        const int last = now.begin + 2 < g.seg_stages ? g.seg_stages - 1 : g.stages - 1;
-        if (last < whole) whole = last;
-      }
+      // (the first half is read again behind the outputs, which need its registers)
+      static_for<READS>([&](auto X) { read_one(X, a0 + (2 * hand - SLOT), b0 + (2 * hand - SLOT), f0); });
       int kt = now.begin;
-      if (kt < whole - 2) {
-        for (; kt < whole - 2; ++kt) stage(kt, std::true_type{});
-        to_kt = whole;
+      while (kt < now.end) {
+        // stages that are copied between products: whole, and of the same piece of K and of work
+        const int piece_end = kt + 2 < g.seg_stages ? g.seg_stages : g.stages;
+        const int stop = piece_end - cut < now.end ? piece_end - cut : now.end;
+        if (kt + 2 < stop) {
+          const At s = at(kt + 2);
+          la.go(s.piece, s.k);
+          lb.go(s.piece, s.k);
+          to_kt = stop;
+          for (; kt + 2 < stop; ++kt) stage(std::true_type{});
+        }
+        stage(std::false_type{});
+        ++kt;
       }
-      for (; kt < now.end; ++kt) stage(kt, std::false_type{});
       wait_vmcnt<0>();
       landed = true;
       out(acc, part, now.m0 + wr * 16, now.n0 + wc * 16, opaque(lane), now.split);
@@ -450,9 +484,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mma(MmaArgs g, Out out) {
       for (int q = 0; q < 2; ++q) {
         v8s_t fa[TM], fb[TN];
 #pragma unroll
-        for (int i = 0; i < TM; ++i) fa[i] = fragment<BM, ADOWN>(slot, wr + i, q, lane);
+        for (int i = 0; i < TM; ++i)
+          fa[i] = Fragments<BM, ADOWN>::read(Fragments<BM, ADOWN>::start(slot, wr, q, lane), wr, i);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) fb[j] = fragment<BN, BDOWN>(slot + LoadA::SIZE, wc + j, q, lane);
+        for (int j = 0; j < TN; ++j)
+          fb[j] = Fragments<BN, BDOWN>::read(Fragments<BN, BDOWN>::start(slot + LoadA::SIZE, wc, q, lane), wc, j);
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll

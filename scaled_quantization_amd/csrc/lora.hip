@@ -6,8 +6,8 @@
 // 32, so that an adapter's weights are read once per tile.  Two kernels follow: the first gathers a
 // tile's tokens and leaves v in binary32, K split over workgroups where there are few tiles; the second adds
 // the ranges up and multiplies by b.  v goes to the matrix instructions as a sum of two 16-bit
-// values, scaled by a power of two per token: 16 ranks fill half of an instruction's 32, so the low parts
-// take the other half and cost nothing.
+// values, scaled by a power of two per token: of up to 16 ranks, which fill half of an instruction's 32, the low parts
+// take the other half; more have an instruction for each part.
 #include "gated_core.hpp"
 
 namespace fp8dp {
@@ -134,6 +134,9 @@ __global__ __launch_bounds__(64 * kPlanWaves) void k_lora_plan(const int32_t* in
   }
 }
 
+// Ranks as the matrix instructions take them.
+__host__ __device__ inline int lora_pitch(int rank) { return rank <= 16 ? 16 : (rank + 31) / 32 * 32; }
+
 struct LoraArgs {
   LoraPlan plan;
   const void *x, *a, *b, *base;
@@ -141,7 +144,7 @@ struct LoraArgs {
   const int32_t* ranks;
   int N, K, rank, adapters, splits, k_range;
   void* y;
-  float* v;   // [split][place][ranks to a multiple of 16]
+  float* v;   // [split][place][lora_pitch(rank)]
 };
 
 __device__ __forceinline__ int lora_rank(const LoraArgs& a, int adapter) {
@@ -155,11 +158,11 @@ __device__ __forceinline__ v8s_t as_lora(const Raw8<T>& r) {
   return __builtin_bit_cast(v8s_t, u32x4_t{r.w[0], r.w[1], r.w[2], r.w[3]});
 }
 
-// v of a tile, up to 16 RB ranks and a range of K; four waves take its blocks of 64 in turn.
-constexpr int kLoraWaves = 4;
+// v of a tile, up to 16 RB ranks and a range of K; eight waves take its blocks of 64 in turn.
+constexpr int kDownWaves = 8, kLoraWaves = 4;   // of the first kernel's workgroups, and of the second's
 template <typename T, int RB>
-__global__ __launch_bounds__(64 * kLoraWaves) void k_lora_down(LoraArgs a) {
-  __shared__ v4f_t sums[kLoraWaves][RB][2][64];
+__global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
+  __shared__ v4f_t sums[kDownWaves][RB][2][64];
   LoraTile tile;
   if (!lora_tile(a.plan, a.adapters, blockIdx.x, &tile) || tile.adapter < 0) return;
   const int rank = lora_rank(a, tile.adapter), r0 = blockIdx.z * 16 * RB;
@@ -207,45 +210,56 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora_down(LoraArgs a) {
       }
   };
   int k0 = begin + wave * 64;
-  for (; k0 + 64 <= end; k0 += kLoraWaves * 64) block(k0, std::true_type{});
+  for (; k0 + 64 <= end; k0 += kDownWaves * 64) block(k0, std::true_type{});
   if (k0 < end) block(k0, std::false_type{});
 #pragma unroll
   for (int b = 0; b < RB; ++b)
 #pragma unroll
     for (int i = 0; i < 2; ++i) sums[wave][b][i][lane] = acc[b][i];
   __syncthreads();
-  const int rp = (a.rank + 15) / 16 * 16;
-  for (int i = threadIdx.x; i < RB * 2 * 64; i += 64 * kLoraWaves) {
+  const int rp = lora_pitch(a.rank);
+  for (int i = threadIdx.x; i < RB * 2 * 64; i += 64 * kDownWaves) {
     const int l = i & 63, half = (i >> 6) & 1, b = i >> 7;
     const int token = 16 * half + (l & 15), r = r0 + 16 * b + 4 * (l >> 4);
     if (token >= tile.count || r >= rp) continue;
     v4f_t s = sums[0][b][half][l];
 #pragma unroll
-    for (int w = 1; w < kLoraWaves; ++w) s += sums[w][b][half][l];
+    for (int w = 1; w < kDownWaves; ++w) s += sums[w][b][half][l];
     *reinterpret_cast<v4f_t*>(a.v + ((int64_t)blockIdx.y * a.plan.tokens + tile.start + token) * rp + r) = s;
   }
 }
 
-// y of a tile and 32 channels a turn of each wave.  v is staged in LDS as 16-bit pairs [token][16 ranks: 16
-// high parts, 16 low parts].  Two instructions give a lane one token and 8 consecutive channels.
-constexpr int kLoraChannels = 512;   // of a workgroup
+// 8 outputs that stay in the caches: 64 bytes of a row are half a cache line, whose other half another wave stores, and
+// past the caches each half is a write of its own.
 template <typename T>
+__device__ __forceinline__ void store_kept(T* p, int n, const float v[8]) {
+  if (n >= 8) *reinterpret_cast<u32x4_e_t*>(p) = round8(v, T{}).w;
+  else store8(p, n, v);
+}
+
+// y of a tile.  A wave takes 32 channels a step; pairs of instructions give a lane one token and 8 consecutive
+// channels.  What a step reads (base and b, up to 16 RB ranks) is loaded DEPTH steps ahead, the first of them
+// before v is there.  v is staged in LDS as 16-bit pairs [token][GR ranks: GR high parts, GR low parts].
+constexpr int kLoraChannels = 512;   // of a workgroup
+constexpr int kLoraSplits = 8;       // most ranges of K
+template <typename T, int RB, int DEPTH>
 __global__ __launch_bounds__(64 * kLoraWaves) void k_lora_up(LoraArgs a) {
-  extern __shared__ __attribute__((aligned(16))) uint16_t pairs[];
+  constexpr int GR = RB == 1 ? 16 : 32, GN = RB == 1 ? 1 : RB / 2;   // ranks of a group, groups of a chunk
+  extern __shared__ __attribute__((aligned(16))) uint8_t shared_up[];
   __shared__ float factor[kLoraTile];
   LoraTile tile;
   if (!lora_tile(a.plan, a.adapters, blockIdx.x, &tile)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rank = tile.adapter < 0 ? 0 : lora_rank(a, tile.adapter);
-  const int n_end = std::min<int>(a.N, (blockIdx.y + 1) * kLoraChannels);
+  const int n_begin = blockIdx.y * kLoraChannels, n_end = std::min<int>(a.N, n_begin + kLoraChannels);
   const int32_t* const order = a.plan.order() + tile.start;
   const T* const base = static_cast<const T*>(a.base);
   T* const y = static_cast<T*>(a.y);
   if (rank == 0) {
     if (y == base) return;
-    const int n = n_end - blockIdx.y * kLoraChannels, vecs = (n + 7) / 8;
+    const int vecs = (n_end - n_begin + 7) / 8;
     for (int i = threadIdx.x; i < tile.count * vecs; i += 64 * kLoraWaves) {
-      const int c = blockIdx.y * kLoraChannels + i % vecs * 8;
+      const int c = n_begin + i % vecs * 8;
       const int64_t at = (int64_t)order[i / vecs] * a.N + c;
       Raw8<T> r = {};
       if (base != nullptr) r = load_raw(base + at, n_end - c);
@@ -253,22 +267,77 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora_up(LoraArgs a) {
     }
     return;
   }
-  const int blocks = (rank + 15) / 16, rp = (a.rank + 15) / 16 * 16, pitch = blocks * 32 + 8;
-  // 8 threads a token
+  const int row = lane & 15, part = lane >> 4;
+  const bool second = tile.count > 16;
+  const int groups = (rank + GR - 1) / GR, chunks = (groups + GN - 1) / GN, wide = groups * GR;
+  auto rank_at = [&](int g) { return g * GR + 8 * (RB == 1 ? part & 1 : part); };   // of this lane's 8 in group g
+  const T* const b = static_cast<const T*>(a.b) + (int64_t)tile.adapter * a.N * a.rank;
+  int64_t token[2];   // first element of this lane's rows of base and y
+  bool live[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    live[i] = 16 * i + row < tile.count;
+    token[i] = (int64_t)order[live[i] ? 16 * i + row : 0] * a.N;
+  }
+  struct Step {
+    Raw8<T> old[2], w[GN][2];
+  };
+  const int turns = (n_end - n_begin - wave * 32 + kLoraWaves * 32 - 1) / (kLoraWaves * 32), steps = turns * chunks;
+  auto load = [&](int s, Step& o) {
+    if (s >= steps) return;
+    const int turn = chunks == 1 ? s : s / chunks, chunk = s - turn * chunks;
+    const int n0 = n_begin + (turn * kLoraWaves + wave) * 32, c = n0 + 8 * part;
+    if (chunk == 0 && base != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (live[i]) o.old[i] = load_raw(base + token[i] + c, n_end - c);
+    }
+    // row i of instruction j is channel 8 (i / 4) + 4 j + i % 4
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int n = n0 + 8 * (row >> 2) + 4 * j + (row & 3);
+      const T* const br = b + (int64_t)(n < a.N ? n : a.N - 1) * a.rank;
+#pragma unroll
+      for (int k = 0; k < GN; ++k) {
+        const int r = rank_at(chunk * GN + k);
+        if (a.rank >= 8) o.w[k][j] = load_raw8(br + (r < a.rank - 8 ? r : a.rank - 8));
+        else load_cut(br, a.rank, o.w[k][j]);
+      }
+    }
+  };
+  Step ahead[DEPTH];
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) {
+    ahead[d] = Step{};
+    load(d, ahead[d]);
+  }
+
+  // v: the ranges' sums in binary32, then the pairs (8 threads a token)
+  const int rp = lora_pitch(a.rank), pitch = wide * 2 + 8;
+  float* const sums = reinterpret_cast<float*>(shared_up);                       // [token][wide]
+  uint16_t* const pairs = reinterpret_cast<uint16_t*>(sums + kLoraTile * wide);
   {
-    const int token = threadIdx.x >> 3, sub = threadIdx.x & 7;
-    const bool live = token < tile.count;
-    const float* const from = a.v + (int64_t)(tile.start + (live ? token : 0)) * rp;
     const int64_t step = (int64_t)a.plan.tokens * rp;
-    auto value = [&](int r) {
-      float s = 0.0f;
-      if (live && r < rank)
-        for (int p = 0; p < a.splits; ++p) s += from[p * step + r];
-      return s;
-    };
+    for (int i = threadIdx.x; i < tile.count * (wide / 4); i += 64 * kLoraWaves) {
+      const int t = i / (wide / 4), r = (i - t * (wide / 4)) * 4;
+      const float* const from = a.v + (int64_t)(tile.start + t) * rp + r;
+      v4f_t s = *reinterpret_cast<const v4f_t*>(from);
+#pragma unroll 7
+      for (int p = 1; p < a.splits; ++p) s += *reinterpret_cast<const v4f_t*>(from + p * step);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (r + j >= rank) s[j] = 0.0f;
+      *reinterpret_cast<v4f_t*>(sums + t * wide + r) = s;
+    }
+  }
+  __syncthreads();
+  {
+    const int t = threadIdx.x >> 3, sub = threadIdx.x & 7;
+    const float* const from = sums + t * wide;
+    const bool mine = t < tile.count;
     float top = 0.0f;
-    for (int r = sub; r < blocks * 16; r += 8) {
-      const float m = __builtin_fabsf(value(r));
+    for (int r = sub; r < wide; r += 8) {
+      const float m = mine ? __builtin_fabsf(from[r]) : 0.0f;
       top = m > top ? m : top;
     }
 #pragma unroll
@@ -281,74 +350,94 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora_up(LoraArgs a) {
     const bool plain = e > 0 && e < 255;
     const int shift = plain ? (e < 2 ? 125 : e > 252 ? -125 : 127 - e) : 0;
     const float down = __uint_as_float((uint32_t)(127 + shift) << 23);
-    for (int r = sub; r < blocks * 16; r += 8) {
-      const float v = value(r) * down;
+    for (int r = sub; r < wide; r += 8) {
+      const float v = mine ? from[r] * down : 0.0f;
       const T hi = from_f32<T>(v);
       const float rest = v - to_f32(hi);
-      uint16_t* const at = pairs + token * pitch + r / 16 * 32 + r % 16;
+      uint16_t* const at = pairs + t * pitch + r / GR * (2 * GR) + r % GR;
       at[0] = hi.bits;
-      at[16] = from_f32<T>(rest == rest ? rest : 0.0f).bits;   // (an infinite v has no low part)
+      at[GR] = from_f32<T>(rest == rest ? rest : 0.0f).bits;   // (an infinite v has no low part)
     }
-    if (sub == 0)
-      factor[token] = a.scale[tile.adapter] * __uint_as_float((uint32_t)(127 - shift) << 23);
+    if (sub == 0) factor[t] = a.scale[tile.adapter] * __uint_as_float((uint32_t)(127 - shift) << 23);
   }
   __syncthreads();
-  const int row = lane & 15, part = lane >> 4;
-  const bool second = tile.count > 16;
-  const T* const b = static_cast<const T*>(a.b) + (int64_t)tile.adapter * a.N * a.rank;
-  for (int n0 = blockIdx.y * kLoraChannels + wave * 32; n0 < n_end; n0 += kLoraWaves * 32) {
-    const int c = n0 + 8 * part, left = n_end - c;
-    int64_t at[2];
-    Raw8<T> old[2] = {};
+
+  v4f_t acc[2][2] = {};
+  Raw8<T> old[2] = {};
+  // A vector of b's ranks r .. r + 7 as read: what is beyond the rank is cleared (it may be anything, and meets zeros).  A row
+  // of b that the vector would leave was read as its last 8.
+  auto settled = [&](Raw8<T> w, int r) {
+    const int from = a.rank < 8 ? 0 : r < a.rank - 8 ? r : a.rank - 8;
+    if (r > from) w.w = shift_down(w.w, 16 * (r - from));
+    const int n = rank - r;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int token = 16 * i + row;
-      at[i] = token < tile.count ? (int64_t)order[token] * a.N + c : -1;
-      if (at[i] >= 0 && base != nullptr) old[i] = load_raw(base + at[i], left);
-    }
-    v4f_t acc[2][2] = {};
-    // row i of instruction j is channel 8 (i / 4) + 4 j + i % 4
-    const T* br[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int n = n0 + 8 * (row >> 2) + 4 * j + (row & 3);
-      br[j] = b + (int64_t)(n < a.N ? n : a.N - 1) * a.rank;
-    }
-    for (int k = 0; k < blocks; ++k) {
-      const int r = 16 * k + 8 * (part & 1);
-      Raw8<T> w[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) w[j] = load_raw(br[j] + r, rank - r);
+    for (int j = 0; j < 4; ++j) w.w[j] &= (2 * j < n ? 0xFFFFu : 0u) | (2 * j + 1 < n ? 0xFFFF0000u : 0u);
+    return w;
+  };
+  auto multiply = [&](int s, const Step& o) {
+    const int turn = chunks == 1 ? s : s / chunks, chunk = s - turn * chunks;
+    if (chunk == 0) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (i == 1 && !second) continue;
-        const uint16_t* const from = pairs + (16 * i + row) * pitch + 32 * k + 8 * part;
-        const v8s_t v = *reinterpret_cast<const v8s_t*>(from);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = mma16(T{}, as_lora(w[j]), v, acc[i][j]);
+        old[i] = o.old[i];
+        acc[i][0] = acc[i][1] = v4f_t{0.0f, 0.0f, 0.0f, 0.0f};
       }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (at[i] < 0 || left <= 0) continue;
-      const float f = factor[16 * i + row];
-      float o[8], s[8];
-      widen8f(old[i], o);
+    for (int k = 0; k < GN; ++k) {
+      const int at = chunk * GN + k;
+      if (at >= groups) break;
+      Raw8<T> w[2] = {o.w[k][0], o.w[k][1]};
+      if (at * GR + GR > rank) {
+        w[0] = settled(w[0], rank_at(at));
+        w[1] = settled(w[1], rank_at(at));
+      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] = __builtin_fmaf(acc[i][j >> 2][j & 3], f, o[j]);
-      store8(y + at[i], left, s);
+      for (int i = 0; i < 2; ++i) {
+        if (i == 1 && !second) continue;
+        const uint16_t* const from = pairs + (16 * i + row) * pitch + 2 * GR * at + 8 * part;
+        // (of 16 ranks the lanes of the upper two parts hold the low parts)
+        const v8s_t hi = *reinterpret_cast<const v8s_t*>(from);
+        v8s_t lo;
+        if constexpr (RB > 1) lo = *reinterpret_cast<const v8s_t*>(from + GR);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          acc[i][j] = mma16(T{}, as_lora(w[j]), hi, acc[i][j]);
+          if constexpr (RB > 1) acc[i][j] = mma16(T{}, as_lora(w[j]), lo, acc[i][j]);
+        }
+      }
+    }
+    if (chunk + 1 < chunks) return;
+    const int c = n_begin + (turn * kLoraWaves + wave) * 32 + 8 * part, left = n_end - c;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (!live[i] || left <= 0) continue;
+      const float f = factor[16 * i + row];
+      float was[8], sum[8];
+      widen8f(old[i], was);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] = __builtin_fmaf(acc[i][j >> 2][j & 3], f, was[j]);
+      store_kept(y + token[i] + c, left, sum);
+    }
+  };
+  for (int s = 0; s < steps; s += DEPTH) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      if (s + d >= steps) break;
+      multiply(s + d, ahead[d]);
+      load(s + d + DEPTH, ahead[d]);
     }
   }
 }
 
-// Over how many ranges K is split: workgroups for every compute unit four times, ranges of 256 or more.
+// Over how many ranges K is split: a workgroup for every compute unit, ranges of 512 or more.
 struct LoraSplit {
   int splits, range;
 };
 static LoraSplit lora_split(int64_t tokens, int64_t K, int64_t rank, int64_t adapters) {
   const int64_t tiles = tokens / kLoraTile + std::min(tokens, adapters), groups = tiles * ((rank + 63) / 64);
   int64_t s = (4 * (int64_t)num_cus() + groups - 1) / groups;
-  s = std::max<int64_t>(1, std::min<int64_t>({s, K / 256, 16}));
+  s = std::max<int64_t>(1, std::min<int64_t>({s, K / 512, kLoraSplits}));
   const int64_t range = round_up((K + s - 1) / s, 64);
   return {(int)((K + range - 1) / range), (int)range};
 }
@@ -359,14 +448,16 @@ static int run_lora(const LoraArgs& a, int64_t most, hipStream_t stream) {
   const int rb = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
   const dim3 block(64 * kLoraWaves);
   const dim3 down((unsigned)most, (unsigned)a.splits, (unsigned)((a.rank + 16 * rb - 1) / (16 * rb)));
-  if (rb == 1) hipLaunchKernelGGL((k_lora_down<T, 1>), down, block, 0, stream, a);
-  else if (rb == 2) hipLaunchKernelGGL((k_lora_down<T, 2>), down, block, 0, stream, a);
-  else hipLaunchKernelGGL((k_lora_down<T, 4>), down, block, 0, stream, a);
+  if (rb == 1) hipLaunchKernelGGL((k_lora_down<T, 1>), down, dim3(64 * kDownWaves), 0, stream, a);
+  else if (rb == 2) hipLaunchKernelGGL((k_lora_down<T, 2>), down, dim3(64 * kDownWaves), 0, stream, a);
+  else hipLaunchKernelGGL((k_lora_down<T, 4>), down, dim3(64 * kDownWaves), 0, stream, a);
   const int rc = check_launch(what);
   if (rc) return rc;
   const dim3 up((unsigned)most, (unsigned)((a.N + kLoraChannels - 1) / kLoraChannels));
-  const size_t lds = (size_t)kLoraTile * ((a.rank + 15) / 16 * 32 + 8) * 2;
-  hipLaunchKernelGGL((k_lora_up<T>), up, block, lds, stream, a);
+  const size_t wide = lora_pitch(a.rank), lds = kLoraTile * (wide * 4 + (wide * 2 + 8) * 2);
+  if (rb == 1) hipLaunchKernelGGL((k_lora_up<T, 1, 4>), up, block, lds, stream, a);
+  else if (rb == 2) hipLaunchKernelGGL((k_lora_up<T, 2, 4>), up, block, lds, stream, a);
+  else hipLaunchKernelGGL((k_lora_up<T, 4, 3>), up, block, lds, stream, a);
   return check_launch(what);
 }
 
@@ -418,7 +509,7 @@ extern "C" int64_t lora_add_workspace(int64_t tokens, int64_t N, int64_t K, int6
   if (!lora_sizes(tokens, adapters) || N < 1 || K < 1 || rank < 1 || N > FP8DP_GATED_MAX_WIDTH ||
       K > FP8DP_GATED_MAX_WIDTH || rank > FP8DP_LORA_MAX_RANK)
     return -1;
-  return (int64_t)lora_split(tokens, K, rank, adapters).splits * tokens * round_up(rank, 16) * 4;
+  return (int64_t)lora_split(tokens, K, rank, adapters).splits * tokens * lora_pitch((int)rank) * 4;
 }
 
 extern "C" int lora_add(const void* x, const void* a, const void* b, const float* scale, const int32_t* ranks,

@@ -102,10 +102,33 @@ __global__ __launch_bounds__(256) void k_gated_join(const float* parts, int spli
 // weight's rows as its first operand, so a lane ends with one token and four channels.  Rows may start and
 // end at any byte: a chunk that K cuts is read as the row's last 8 values and shifted.
 constexpr int kFewWaves = 8, kFewTokens16 = 64;
+constexpr int64_t kRingWork = (int64_t)256 * 1024;   // groups of 16 channels x K from which on rings are used
 
 template <typename T>
 __device__ __forceinline__ v8s_t as_frag(const Raw8<T>& r) {
   return __builtin_bit_cast(v8s_t, u32x4_t{r.w[0], r.w[1], r.w[2], r.w[3]});
+}
+
+// Outputs of one token and four channels c0 ..
+template <typename T>
+__device__ __forceinline__ void store_few(v4f_t g, v4f_t u, int token, int c0, int M, int N, int act, T* h, T* gate,
+                                          T* up) {
+  if (token >= M) return;
+  float v[4];
+  with_act(act, [&](auto ACT) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = gate_of<decltype(ACT)::value, false>(g[r], nullptr) * u[r];
+  });
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (c0 + r >= N) continue;
+    const int64_t at = (int64_t)token * N + c0 + r;
+    h[at] = from_f32<T>(v[r]);
+    if (gate != nullptr) {
+      gate[at] = from_f32<T>(g[r]);
+      up[at] = from_f32<T>(u[r]);
+    }
+  }
 }
 
 template <typename T, int MT>
@@ -165,22 +188,117 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(const T* x, const 
     g += sums[w][0][wave][lane];
     u += sums[w][1][wave][lane];
   }
-  const int token = 16 * wave + row;
-  if (token >= M) return;
-  float v[4];
-  with_act(act, [&](auto ACT) {
+  store_few(g, u, 16 * wave + row, n0 + 4 * part, M, N, act, h, gate, up);
+}
+
+// The same for rows that start at multiples of 16 bytes.  Fragments read straight from memory have 16 rows in consecutive
+// lanes, which the compute unit takes one 16-byte piece a cycle; here each wave copies whole cache lines into a ring of its
+// own in LDS, 8 rows x 128 bytes a copy, four times the rate (48 tokens x 16384 x 4096: 85 -> 47 us).  Stages of 64 k go to the waves
+// in turn; the grid is resident, and a wave's ring runs on into the workgroup's next 16 channels while their sums
+// are joined.  W waves and S slots: 64 KiB or more under way in each compute unit.
+template <typename T, int MT, int W, int S>
+__global__ __launch_bounds__(64 * W) void k_gated_ring(const T* x, const T* w_gate, const T* w_up, int M, int N,
+                                                       int K, int act, T* h, T* gate, T* up) {
+  constexpr int TILES = 2 + MT, STAGE = TILES * 2048, NC = 2 * TILES;   // tiles of 16 rows x 64 k; copies a stage
+  __shared__ __attribute__((aligned(1024))) uint8_t rings[W * S * STAGE];
+  __shared__ v4f_t sums[W][2][MT][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint8_t* const ring = rings + wave * S * STAGE;
+  const int row = lane & 15, part = lane >> 4;
+  const int stages = (K + kStageK - 1) / kStageK, mine = stages > wave ? (stages - wave + W - 1) / W : 0;
+  const int groups = (N + 15) / 16, turns = ((int)gridDim.x + groups - 1 - (int)blockIdx.x) / (int)gridDim.x;
+  // copy c of a stage: rows 8 (c % 2) + lane / 8 of tile c / 2, the chunk that swz() puts there
+  const int crow = lane >> 3, cchunk = lane & 7;
+  uint32_t xoff[2 * MT];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = gate_of<decltype(ACT)::value, false>(g[r], nullptr) * u[r];
-  });
+  for (int c = 0; c < 2 * MT; ++c) {
+    const int r = 16 * (c / 2) + 8 * (c % 2) + crow;
+    xoff[c] = (uint32_t)(r < M ? r : M - 1) * (uint32_t)K * 2;
+  }
+  int to = blockIdx.x, to_stage = 0;   // the next to be copied: the group's channels, and its place among this wave's
+  auto issue = [&](int slot) {
+    const int k0 = (wave + to_stage * W) * kStageK, left = K - k0;
+    static_for<NC>([&](auto C) {
+      constexpr int c = decltype(C)::value, tile = c / 2;
+      const int chunk = cchunk ^ ((4 * (c % 2) + (crow >> 1)) & 7);
+      const T* base;
+      uint32_t from;
+      if constexpr (tile < 2) {
+        const int n = to * 16 + 8 * (c % 2) + crow;
+        base = (tile == 0 ? w_gate : w_up) + (int64_t)to * 16 * K + k0;
+        from = (uint32_t)((n < N ? n : N - 1) - to * 16) * (uint32_t)K * 2;
+      } else {
+        base = x + k0;
+        from = xoff[c - 4];
+      }
+      from += chunk * 16;
+      uint8_t* const l = ring + slot * STAGE + c * 1024;
+      if (left >= kStageK)
+        copy16_to_lds_from(base, from, l);
+      else
+        copy16_to_lds(chunk * 8 < left ? reinterpret_cast<const uint8_t*>(base) + from
+                                       : reinterpret_cast<const uint8_t*>(&kZeroChunk16), l);
+    });
+    if (++to_stage == mine) {
+      to_stage = 0;
+      to += gridDim.x;
+    }
+  };
+  const int total = mine * turns;   // stages of this wave
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int c = n0 + 4 * part + r;
-    if (c >= N) continue;
-    const int64_t at = (int64_t)token * N + c;
-    h[at] = from_f32<T>(v[r]);
-    if (gate != nullptr) {
-      gate[at] = from_f32<T>(g[r]);
-      up[at] = from_f32<T>(u[r]);
+  for (int s = 0; s < S - 1; ++s)
+    if (s < total) issue(s);
+  int at = 0, slot = 0;             // the stage in hand
+  for (int group = blockIdx.x; group < groups; group += gridDim.x) {
+    v4f_t ag[MT], au[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) ag[i] = au[i] = v4f_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < mine; ++j, ++at) {
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the slot to be filled has been read
+      if (at + S - 1 < total) issue(slot == 0 ? S - 1 : slot - 1);
+      // the copies of the stage in hand have landed: of those behind it as many may be under way as there are
+      const int behind = total - 1 - at;
+      if (behind >= S - 1) wait_vmcnt<(S - 1) * NC>();
+      else if (S > 2 && behind == S - 2) wait_vmcnt<(S - 2) * NC>();
+      else if (S > 3 && behind == S - 3) wait_vmcnt<(S > 3 ? S - 3 : 0) * NC>();
+      else wait_vmcnt<0>();
+      __builtin_amdgcn_sched_barrier(0);
+      __asm__ volatile("" ::: "memory");
+      const uint8_t* const from = ring + slot * STAGE;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int f = swz(row, 4 * q + part);
+        const v8s_t g = *reinterpret_cast<const v8s_t*>(from + f), u = *reinterpret_cast<const v8s_t*>(from + 2048 + f);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const v8s_t v = *reinterpret_cast<const v8s_t*>(from + (2 + i) * 2048 + f);
+          ag[i] = mma16(T{}, g, v, ag[i]);
+          au[i] = mma16(T{}, u, v, au[i]);
+        }
+      }
+      slot = slot == S - 1 ? 0 : slot + 1;
+    }
+    // (barriers alone, not __syncthreads(): the copies under way stay so)
+    if (group != (int)blockIdx.x) {   // the sums of the channels before have been read
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      stage_barrier();
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      sums[wave][0][i][lane] = ag[i];
+      sums[wave][1][i][lane] = au[i];
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    stage_barrier();
+    if (wave < MT) {
+      v4f_t g = {0.0f, 0.0f, 0.0f, 0.0f}, u = g;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        g += sums[w][0][wave][lane];
+        u += sums[w][1][wave][lane];
+      }
+      store_few(g, u, 16 * wave + row, group * 16 + 4 * part, M, N, act, h, gate, up);
     }
   }
 }
@@ -215,8 +333,29 @@ static int launch_gated(const char* what, MmaArgs g, int M, int N, int splits, i
 template <typename T>
 static int run_gated(const char* what, const T* x, const T* wg, const T* wu, int M, int N, int K, int act, T* h,
                      T* gate, T* up, float* parts, int64_t parts_bytes, hipStream_t stream) {
+  MmaArgs g = {};
+  g.a = {{reinterpret_cast<const uint16_t*>(x), reinterpret_cast<const uint16_t*>(x)}, K, M};
+  g.b = {{reinterpret_cast<const uint16_t*>(wg), reinterpret_cast<const uint16_t*>(wu)}, K, N};
+  g.stages = g.seg_stages = (K + kStageK - 1) / kStageK;
+  g.valid_a = g.valid_b = K;
+  const bool direct = rows16(g.a, K) && rows16(g.b, K);
   if (M <= kFewTokens16) {
-    const dim3 grid((unsigned)((N + 15) / 16)), block(64 * kFewWaves);
+    const int64_t groups = ((int64_t)N + 15) / 16;
+    if (direct && K >= 256 && groups * K >= kRingWork) {
+      const dim3 grid((unsigned)std::min<int64_t>(groups, num_cus()));
+      auto ring = [&](auto mt, auto w, auto s) {
+        constexpr int W = decltype(w)::value;
+        hipLaunchKernelGGL((k_gated_ring<T, decltype(mt)::value, W, decltype(s)::value>), grid, dim3(64 * W), 0, stream,
+                           x, wg, wu, M, N, K, act, h, gate, up);
+        return check_launch(what);
+      };
+      using std::integral_constant;
+      if (M <= 16) return ring(integral_constant<int, 1>{}, integral_constant<int, 8>{}, integral_constant<int, 3>{});
+      if (M <= 32) return ring(integral_constant<int, 2>{}, integral_constant<int, 4>{}, integral_constant<int, 4>{});
+      if (M <= 48) return ring(integral_constant<int, 3>{}, integral_constant<int, 4>{}, integral_constant<int, 3>{});
+      return ring(integral_constant<int, 4>{}, integral_constant<int, 4>{}, integral_constant<int, 2>{});
+    }
+    const dim3 grid((unsigned)groups), block(64 * kFewWaves);
     auto few = [&](auto mt) {
       hipLaunchKernelGGL((k_gated_few<T, decltype(mt)::value>), grid, block, 0, stream, x, wg, wu, M, N, K, act,
                          h, gate, up);
@@ -227,12 +366,6 @@ static int run_gated(const char* what, const T* x, const T* wg, const T* wu, int
     if (M <= 48) return few(std::integral_constant<int, 3>{});
     return few(std::integral_constant<int, 4>{});
   }
-  MmaArgs g = {};
-  g.a = {{reinterpret_cast<const uint16_t*>(x), reinterpret_cast<const uint16_t*>(x)}, K, M};
-  g.b = {{reinterpret_cast<const uint16_t*>(wg), reinterpret_cast<const uint16_t*>(wu)}, K, N};
-  g.stages = g.seg_stages = (K + kStageK - 1) / kStageK;
-  g.valid_a = g.valid_b = K;
-  const bool direct = rows16(g.a, K) && rows16(g.b, K);
   ProductPlan p = plan_gated(M, N, K, direct);
   if ((int64_t)p.splits * 2 * M * N * 4 > parts_bytes) p.splits = 1;
   int rc;

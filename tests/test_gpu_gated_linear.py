@@ -102,6 +102,15 @@ def test_forward_activations(act, M):
     forward(M, 72, 136, BF16, act, M != 40)
 
 
+@pytest.mark.parametrize("M", [1, 16, 17, 32, 33, 48, 49, 64])
+def test_forward_few_tokens_and_many_weights(M):
+    # rings of weights: fewer groups of channels than workgroups, more of them, stages that K cuts
+    forward(M, 1100, 4104, BF16, "silu", M % 2 == 0)
+    forward(M, 4500, 1000, F16, "gelu_tanh", M % 2 == 1)
+    forward(M, 4112, 1024, BF16, "relu", False)
+    forward(M, 16400, 264, F16, "silu", False)
+
+
 def test_forward_large_tiles_and_no_workspace():
     forward(2048, 4096, 128, BF16, "silu", True)
     forward(2111, 4200, 72, F16, "gelu_tanh", False)

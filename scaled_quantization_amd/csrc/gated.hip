@@ -308,22 +308,22 @@ static ProductPlan plan_gated(int64_t M, int64_t N, int64_t K, bool direct) {
   return plan_product(M, 2 * N, (K + kStageK - 1) / kStageK, true, direct);
 }
 
-template <typename T, int WM, int WN, int TM, int TN, bool DIRECT>
+template <typename T, int WM, int WN, int TM, int TN, int S, bool DIRECT>
 static int launch_gated(const char* what, MmaArgs g, int M, int N, int splits, int act, T* h, T* gate, T* up,
                         float* parts, hipStream_t stream) {
   g.tiles_m = (M + WM * TM * 16 - 1) / (WM * TM * 16);
   g.tiles_n = (N + WN * TN * 8 - 1) / (WN * TN * 8);
   g.splits = splits;
-  return for_work<DIRECT>((int64_t)g.tiles_m * g.tiles_n * splits, WM * WN == 8 ? 1 : 2, [&](int first, unsigned count) {
+  return for_work<DIRECT>((int64_t)g.tiles_m * g.tiles_n * splits, WM * WN == 8 || S > 2 ? 1 : 2, [&](int first, unsigned count) {
     g.first = first;
     const dim3 grid(count), block(64 * WM * WN);
     if (splits > 1) {
       const GatedParts<TM, TN> out = {parts, M, N};
-      hipLaunchKernelGGL((k_mma<T, WM, WN, TM, TN, false, false, true, DIRECT, GatedParts<TM, TN>>), grid,
+      hipLaunchKernelGGL((k_mma<T, WM, WN, TM, TN, S, false, false, true, DIRECT, GatedParts<TM, TN>>), grid,
                          block, 0, stream, g, out);
     } else {
       const GatedOut<T, TM, TN> out = {h, gate, up, M, N, act};
-      hipLaunchKernelGGL((k_mma<T, WM, WN, TM, TN, false, false, true, DIRECT, GatedOut<T, TM, TN>>), grid,
+      hipLaunchKernelGGL((k_mma<T, WM, WN, TM, TN, S, false, false, true, DIRECT, GatedOut<T, TM, TN>>), grid,
                          block, 0, stream, g, out);
     }
     return check_launch(what);
@@ -338,7 +338,7 @@ static int run_gated(const char* what, const T* x, const T* wg, const T* wu, int
   g.b = {{reinterpret_cast<const uint16_t*>(wg), reinterpret_cast<const uint16_t*>(wu)}, K, N};
   g.stages = g.seg_stages = (K + kStageK - 1) / kStageK;
   g.valid_a = g.valid_b = K;
-  const bool direct = rows16(g.a, K) && rows16(g.b, K);
+  bool direct = rows16(g.a, K) && rows16(g.b, K);
   if (M <= kFewTokens16) {
     const int64_t groups = ((int64_t)N + 15) / 16;
     if (direct && K >= 256 && groups * K >= kRingWork) {
@@ -366,12 +366,25 @@ static int run_gated(const char* what, const T* x, const T* wg, const T* wu, int
     if (M <= 48) return few(std::integral_constant<int, 3>{});
     return few(std::integral_constant<int, 4>{});
   }
+  if (!direct && pad_pays(M, N, K, false) && parts_bytes >= pad_bytes(M, N, K)) {
+    uint16_t* const to = reinterpret_cast<uint16_t*>(parts);
+    const int rc = pad_operands(what, g.a.p[0], g.b.p[0], g.b.p[1], M, N, K, to, stream);
+    if (rc) return rc;
+    const int64_t ld = pad_ld(K);
+    g.a = {{to, to}, ld, M};
+    g.b = {{to + M * ld, to + (M + N) * ld}, ld, N};
+    direct = true;
+    parts += pad_bytes(M, N, K) / 4;
+    parts_bytes -= pad_bytes(M, N, K);
+  }
   ProductPlan p = plan_gated(M, N, K, direct);
   if ((int64_t)p.splits * 2 * M * N * 4 > parts_bytes) p.splits = 1;
   int rc;
-  if (p.shape == kTile256) rc = launch_gated<T, 4, 2, 4, 8, true>(what, g, M, N, p.splits, act, h, gate, up, parts, stream);
-  else if (direct) rc = launch_gated<T, 2, 2, 4, 4, true>(what, g, M, N, p.splits, act, h, gate, up, parts, stream);
-  else rc = launch_gated<T, 2, 2, 4, 4, false>(what, g, M, N, p.splits, act, h, gate, up, parts, stream);
+  if (p.shape == kTile256) rc = launch_gated<T, 4, 2, 4, 8, 2, true>(what, g, M, N, p.splits, act, h, gate, up, parts, stream);
+  else if (direct && tiles_of(kTile128, M, 2 * (int64_t)N) * p.splits <= num_cus())
+    rc = launch_gated<T, 2, 2, 4, 4, 4, true>(what, g, M, N, p.splits, act, h, gate, up, parts, stream);
+  else if (direct) rc = launch_gated<T, 2, 2, 4, 4, 2, true>(what, g, M, N, p.splits, act, h, gate, up, parts, stream);
+  else rc = launch_gated<T, 2, 2, 4, 4, 2, false>(what, g, M, N, p.splits, act, h, gate, up, parts, stream);
   if (rc || p.splits == 1) return rc;
   const int64_t total = (int64_t)M * N;
   hipLaunchKernelGGL((k_gated_join<T>), dim3(grid_for((total + 7) / 8, 256, 16)), dim3(256), 0, stream, parts,
@@ -387,8 +400,12 @@ extern "C" int64_t gated_linear_workspace(int64_t M, int64_t N, int64_t K) {
   if (M <= kFewTokens16 || N < 1 || K < 1 || M > FP8DP_GATED_MAX_ROWS || N > FP8DP_GATED_MAX_WIDTH ||
       K > FP8DP_GATED_MAX_WIDTH)
     return 0;
-  const int splits = std::max(plan_gated(M, N, K, true).splits, plan_gated(M, N, K, false).splits);
-  return splits > 1 ? (int64_t)splits * 2 * M * N * 4 : 0;
+  auto parts = [&](bool direct) {
+    const int splits = plan_gated(M, N, K, direct).splits;
+    return splits > 1 ? (int64_t)splits * 2 * M * N * 4 : (int64_t)0;
+  };
+  const int64_t padded = pad_pays(M, N, K, false) ? pad_bytes(M, N, K) + parts(true) : 0;
+  return std::max({padded, parts(false), K % 8 == 0 ? parts(true) : (int64_t)0});
 }
 
 extern "C" int gated_linear(const void* x, const void* w_gate, const void* w_up, int64_t M, int64_t N,

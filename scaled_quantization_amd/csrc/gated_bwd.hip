@@ -1,5 +1,6 @@
 // gated_bwd.hip -- gradients of the gated linear layer.
 //
+//   (x and the weights copied to aligned rows where K is no multiple of 8)
 //   dg = dh u f'(g), du = dh f(g)          one pass, D = [dg | du] of the operands' type
 //   dx = dg Wg + du Wu = D [Wg; Wu]        contraction over the channels, W lies down
 //   [dWg; dWu] = D^T x                     contraction over the tokens, both operands lie down
@@ -118,22 +119,22 @@ __global__ __launch_bounds__(256) void k_plain_join(const float* parts, int spli
   }
 }
 
-template <typename T, int WM, int WN, int TM, int TN, bool ADOWN, bool DIRECT>
+template <typename T, int WM, int WN, int TM, int TN, int S, bool ADOWN, bool DIRECT>
 static int launch_plain(const char* what, MmaArgs g, int m, int splits, Rows2<T> rows, float* parts,
                         hipStream_t stream) {
   g.tiles_m = (m + WM * TM * 16 - 1) / (WM * TM * 16);
   g.tiles_n = (rows.N + WN * TN * 16 - 1) / (WN * TN * 16);
   g.splits = splits;
-  return for_work<DIRECT>((int64_t)g.tiles_m * g.tiles_n * splits, WM * WN == 8 ? 1 : 2, [&](int first, unsigned count) {
+  return for_work<DIRECT>((int64_t)g.tiles_m * g.tiles_n * splits, WM * WN == 8 || S > 2 ? 1 : 2, [&](int first, unsigned count) {
     g.first = first;
     const dim3 grid(count), block(64 * WM * WN);
     if (splits > 1) {
       const PlainParts<TM, TN> out = {parts, m, rows.N};
-      hipLaunchKernelGGL((k_mma<T, WM, WN, TM, TN, ADOWN, true, false, DIRECT, PlainParts<TM, TN>>), grid,
+      hipLaunchKernelGGL((k_mma<T, WM, WN, TM, TN, S, ADOWN, true, false, DIRECT, PlainParts<TM, TN>>), grid,
                          block, 0, stream, g, out);
     } else {
       const PlainOut<T, TM, TN> out = {rows};
-      hipLaunchKernelGGL((k_mma<T, WM, WN, TM, TN, ADOWN, true, false, DIRECT, PlainOut<T, TM, TN>>), grid,
+      hipLaunchKernelGGL((k_mma<T, WM, WN, TM, TN, S, ADOWN, true, false, DIRECT, PlainOut<T, TM, TN>>), grid,
                          block, 0, stream, g, out);
     }
     return check_launch(what);
@@ -145,10 +146,12 @@ template <typename T, bool ADOWN>
 static int run_product(const char* what, const MmaArgs& g, int m, const ProductPlan& p, Rows2<T> rows,
                        float* parts, hipStream_t stream) {
   int rc;
-  if (p.shape == kTile256) rc = launch_plain<T, 4, 2, 4, 8, ADOWN, true>(what, g, m, p.splits, rows, parts, stream);
-  else if (p.shape == kTile192) rc = launch_plain<T, 4, 2, 4, 6, ADOWN, true>(what, g, m, p.splits, rows, parts, stream);
-  else if (p.shape == kTile128) rc = launch_plain<T, 2, 2, 4, 4, ADOWN, true>(what, g, m, p.splits, rows, parts, stream);
-  else rc = launch_plain<T, 2, 2, 4, 4, ADOWN, false>(what, g, m, p.splits, rows, parts, stream);
+  if (p.shape == kTile256) rc = launch_plain<T, 4, 2, 4, 8, 2, ADOWN, true>(what, g, m, p.splits, rows, parts, stream);
+  else if (p.shape == kTile192) rc = launch_plain<T, 4, 2, 4, 6, 2, ADOWN, true>(what, g, m, p.splits, rows, parts, stream);
+  else if (p.shape == kTile128 && tiles_of(kTile128, m, rows.N) * p.splits <= num_cus())
+    rc = launch_plain<T, 2, 2, 4, 4, 4, ADOWN, true>(what, g, m, p.splits, rows, parts, stream);
+  else if (p.shape == kTile128) rc = launch_plain<T, 2, 2, 4, 4, 2, ADOWN, true>(what, g, m, p.splits, rows, parts, stream);
+  else rc = launch_plain<T, 2, 2, 4, 4, 2, ADOWN, false>(what, g, m, p.splits, rows, parts, stream);
   if (rc || p.splits == 1) return rc;
   const int64_t nvec = ((int64_t)rows.N + 7) / 8;
   hipLaunchKernelGGL((k_plain_join<T>), dim3(grid_for(m * nvec, 256, 16)), dim3(256), 0, stream, parts, p.splits,
@@ -175,7 +178,17 @@ static int run_gated_bwd(const char* what, const T* dh, const T* gate, const T* 
                          hipStream_t stream) {
   auto words = [](const T* p) { return reinterpret_cast<const uint16_t*>(p); };
   Operand w = {{words(wg), words(wu)}, K, K}, xs = {{words(x), words(x)}, K, K};
-  const bool direct_w = rows16(w, K), direct_x = rows16(xs, K);
+  bool direct_w = rows16(w, K), direct_x = rows16(xs, K);
+  if (pad_pays(M, N, K, true)) {   // (columns of zeros behind K are multiplied and not stored)
+    uint16_t* const to = static_cast<uint16_t*>(workspace);
+    const int rc = pad_operands(what, xs.p[0], w.p[0], w.p[1], M, N, K, to, stream);
+    if (rc) return rc;
+    const int64_t ld = pad_ld(K);
+    xs = {{to, to}, ld, (int)ld};
+    w = {{to + M * ld, to + (M + N) * ld}, ld, (int)ld};
+    direct_w = direct_x = true;
+    workspace = static_cast<uint8_t*>(workspace) + pad_bytes(M, N, K);
+  }
   const BwdSizes sw(M, N, K, direct_w), sx(M, N, K, direct_x);
   const int Np = (int)sw.Np, Mp = (int)sw.Mp;
   T* const d = static_cast<T*>(workspace);
@@ -218,7 +231,7 @@ extern "C" int64_t gated_linear_backward_workspace(int64_t M, int64_t N, int64_t
       K > FP8DP_GATED_MAX_WIDTH)
     return 0;
   const BwdSizes d(M, N, K, true), a(M, N, K, false);
-  return d.d_bytes + std::max(d.parts_bytes(M, K), a.parts_bytes(M, K));
+  return (pad_pays(M, N, K, true) ? pad_bytes(M, N, K) : 0) + d.d_bytes + std::max(d.parts_bytes(M, K), a.parts_bytes(M, K));
 }
 
 extern "C" int gated_linear_backward(const void* dh, const void* gate, const void* up, const void* x,

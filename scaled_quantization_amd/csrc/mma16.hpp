@@ -275,7 +275,8 @@ struct Fragments {
 // A piece of work is a tile and a range of K, of which there are `splits`.
 // out(acc, LDS of the wave, m of the wave, n of the wave, lane, split): stores the tile.
 //
-// DIRECT: two LDS slots filled by copies that pass no registers.  A stage goes in halves, with
+// DIRECT: S LDS slots filled by copies that pass no registers, two for the large tiles (64 KiB a stage), four where a
+// compute unit has one small tile and its stages would wait for memory.  A stage goes in halves, with
 // fragments double-buffered: the first half of a stage is multiplied while its second is read, then one barrier
 // shows that all copies of the next stage have landed and that this slot has been read; the second
 // half is multiplied while the slot is refilled and the next stage's first half is read.  The copies are
@@ -295,19 +296,19 @@ __device__ __forceinline__ int work_of(int i, int n, int grid) {
   return pass * grid + (left % 8 == 0 ? b % 8 * (left / 8) + b / 8 : b);
 }
 
-template <typename T, int WM, int WN, int TM, int TN, bool ADOWN, bool BDOWN, bool DUAL, bool DIRECT,
+template <typename T, int WM, int WN, int TM, int TN, int S, bool ADOWN, bool BDOWN, bool DUAL, bool DIRECT,
           typename Out>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_mma(MmaArgs g, Out out) {
   constexpr int W = WM * WN, BM = WM * TM * 16, BN = WN * TN * 16;
   using LoadA = Loader<T, BM, W, ADOWN, false, DIRECT>;
   using LoadB = Loader<T, BN, W, BDOWN, DUAL, DIRECT>;
   constexpr int SLOT = LoadA::SIZE + LoadB::SIZE, NCOPY = LoadA::L + LoadB::L;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * SLOT + W * kOutBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * SLOT + W * kOutBytes];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / WN * TM, wc = wave % WN * TN;   // in tiles of 16
-  uint8_t* const part = lds + 2 * SLOT + wave * kOutBytes;
+  uint8_t* const part = lds + S * SLOT + wave * kOutBytes;
   const int ntiles = g.tiles_m * g.tiles_n, total = ntiles * g.splits;
 
   struct Work {
@@ -352,7 +353,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mma(MmaArgs g, Out out) {
     struct Frags {
       v8s_t a[TM], b[TN];
     };
-    // addresses of the second halves in the slot in hand, and of the first halves in the other one
+    // addresses of the second halves in the slot in hand, and of the first halves in the next one
     uint32_t a1 = FragA::start(lds, wr, 1, lane), b1 = FragB::start(lds + LoadA::SIZE, wc, 1, lane);
     uint32_t a0 = FragA::start(lds + SLOT, wr, 0, lane), b0 = FragB::start(lds + SLOT + LoadA::SIZE, wc, 0, lane);
     auto read_one = [&](auto X, uint32_t a, uint32_t b, Frags& f) {
@@ -372,8 +373,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mma(MmaArgs g, Out out) {
         __builtin_amdgcn_sched_barrier(0);
       });
     };
-    // the stage to be copied next: to_kt of piece of work `to`, two stages ahead of the one that is multiplied
+    // the stage to be copied next: to_kt of piece of work `to`, S stages ahead of the one that is multiplied
     int to = blockIdx.x, to_kt = 0, to_end = 0;
+    int later = -1;   // stages that have been copied or are under way behind the one in hand
+
     auto issue = [&](uint8_t* slot, bool first) {
       if (first || to_kt == to_end) {   // on to the next piece of work
         if (!first) to += gridDim.x;
@@ -389,15 +392,22 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mma(MmaArgs g, Out out) {
       lb.go(s.piece, s.k);
       la.copy(g.valid_a - s.k, slot);
       lb.copy(g.valid_b - s.k, slot + LoadA::SIZE);
+      ++later;
     };
 #pragma unroll 1
-    for (int s = 0; s < 2; ++s) issue(lds + s * SLOT, s == 0);
-    if (to < total) wait_vmcnt<NCOPY>();
-    else wait_vmcnt<0>();
+    for (int s = 0; s < S; ++s) issue(lds + s * SLOT, s == 0);
+    // all but the copies of the last `n` stages have landed
+    auto landed_but = [&](int n) {
+      if (S > 3 && n >= 3) wait_vmcnt<(S > 3 ? 3 : 0) * NCOPY>();
+      else if (S > 2 && n == 2) wait_vmcnt<(S > 2 ? 2 : 0) * NCOPY>();
+      else if (n == 1) wait_vmcnt<NCOPY>();
+      else wait_vmcnt<0>();
+    };
+    landed_but(later);
     stage_barrier();
     Frags f0, f1;
-    uint32_t hand = 0;     // the slot of the stage in hand, in bytes
-    bool landed = false;   // the copies of the stage behind it have been waited for
+    uint32_t hand = 0, next = SLOT;   // the slots of the stage in hand and of the next one, in bytes
+    int landed = 0;                   // stages behind the one in hand that have been waited for
     // One stage.  COPY: the stage to be copied is whole and the one behind the last copied, and copied between the
     // products; else it is any, or none, and copied ahead of them.  The next stage's first half is read even where
     // there is no next stage: nothing looks at it then.
@@ -408,10 +418,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mma(MmaArgs g, Out out) {
         if constexpr (decltype(X)::value < READS) read_one(X, a1, b1, f1);
       });
       __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's reads of the stage are done
-      if (!landed) wait_vmcnt<0>();         // its copies of the next one have landed
-      landed = false;
+      // its copies of the next one have landed
+      if (landed > 0) --landed;
+      else if constexpr (copy) wait_vmcnt<(S - 2) * NCOPY>();
+      else landed_but(later - 1);
       stage_barrier();
-      if constexpr (!copy) issue(slot, false);
+      if constexpr (!copy) {
+        issue(slot, false);
+        --later;
+      }
       multiply(f1, [&](auto X) {
         constexpr int x = decltype(X)::value, c0 = x * NCOPY / PRODUCTS, c1 = (x + 1) * NCOPY / PRODUCTS;
         if constexpr (x < READS) read_one(X, a0, b0, f0);
@@ -427,36 +442,37 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mma(MmaArgs g, Out out) {
         la.step();
         lb.step();
       }
-      const uint32_t over = SLOT - 2 * hand;   // to the other slot
-      a1 += over;
-      b1 += over;
-      a0 -= over;
-      b0 -= over;
-      hand += over;
+      const uint32_t after = next + SLOT == S * SLOT ? 0 : next + SLOT;
+      a1 += next - hand;
+      b1 += next - hand;
+      a0 += after - next;
+      b0 += after - next;
+      hand = next;
+      next = after;
     };
     const int least = g.valid_a < g.valid_b ? g.valid_a : g.valid_b;
     const int cut = least < g.seg_stages * kStageK ? 1 : 0;   // the last stage of a piece of K is not whole
     for (int i = blockIdx.x; i < total; i += gridDim.x) {
       const Work now = work(i);
       // (the first half is read again behind the outputs, which need its registers)
-      static_for<READS>([&](auto X) { read_one(X, a0 + (2 * hand - SLOT), b0 + (2 * hand - SLOT), f0); });
+      static_for<READS>([&](auto X) { read_one(X, a0 + (hand - next), b0 + (hand - next), f0); });
       int kt = now.begin;
       while (kt < now.end) {
         // stages that are copied between products: whole, and of the same piece of K and of work
-        const int piece_end = kt + 2 < g.seg_stages ? g.seg_stages : g.stages;
+        const int piece_end = kt + S < g.seg_stages ? g.seg_stages : g.stages;
         const int stop = piece_end - cut < now.end ? piece_end - cut : now.end;
-        if (kt + 2 < stop) {
-          const At s = at(kt + 2);
+        if (kt + S < stop) {
+          const At s = at(kt + S);
           la.go(s.piece, s.k);
           lb.go(s.piece, s.k);
           to_kt = stop;
-          for (; kt + 2 < stop; ++kt) stage(std::true_type{});
+          for (; kt + S < stop; ++kt) stage(std::true_type{});
         }
         stage(std::false_type{});
         ++kt;
       }
       wait_vmcnt<0>();
-      landed = true;
+      landed = S - 1;
       out(acc, part, now.m0 + wr * 16, now.n0 + wc * 16, opaque(lane), now.split);
       clear();
     }

@@ -31,12 +31,13 @@ struct LoraTile {
 };
 // Whether workgroup `b` has a tile of a plan for these sizes.
 __device__ __forceinline__ bool lora_tile(const LoraPlan& plan, int adapters, int b, LoraTile* t) {
-  if (plan.p[1] != plan.tokens || plan.p[2] != adapters || b >= plan.p[0]) return false;
+  // (the entry is there for every workgroup, and read along with the head)
   const int32_t* const e = plan.tiles() + 2 * (int64_t)b;
-  t->start = e[0];
-  t->adapter = e[1] >> 8;
-  t->count = e[1] & 255;
-  return true;
+  const int start = e[0], info = e[1], count = plan.p[0], tokens = plan.p[1], made_for = plan.p[2];
+  t->start = start;
+  t->adapter = info >> 8;
+  t->count = info & 255;
+  return tokens == plan.tokens && made_for == adapters && b < count;
 }
 
 // One workgroup: counts per wave and adapter in LDS (each wave has a range of the tokens), their sums over
@@ -240,10 +241,10 @@ __device__ __forceinline__ void store_kept(T* p, int n, const float v[8]) {
 // y of a tile.  A wave takes 32 channels a step; pairs of instructions give a lane one token and 8 consecutive
 // channels.  What a step reads (base and b, up to 16 RB ranks) is loaded DEPTH steps ahead, the first of them
 // before v is there.  v is staged in LDS as 16-bit pairs [token][GR ranks: GR high parts, GR low parts].
-constexpr int kLoraChannels = 512;   // of a workgroup
+constexpr int kLoraChannels = 512;   // of a workgroup (64 lanes x 8)
 constexpr int kLoraSplits = 8;       // most ranges of K
 template <typename T, int RB, int DEPTH>
-__global__ __launch_bounds__(64 * kLoraWaves) void k_lora_up(LoraArgs a) {
+__global__ __launch_bounds__(64 * kLoraWaves, 4) void k_lora_up(LoraArgs a) {
   constexpr int GR = RB == 1 ? 16 : 32, GN = RB == 1 ? 1 : RB / 2;   // ranks of a group, groups of a chunk
   extern __shared__ __attribute__((aligned(16))) uint8_t shared_up[];
   __shared__ float factor[kLoraTile];
@@ -257,13 +258,20 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora_up(LoraArgs a) {
   T* const y = static_cast<T*>(a.y);
   if (rank == 0) {
     if (y == base) return;
-    const int vecs = (n_end - n_begin + 7) / 8;
-    for (int i = threadIdx.x; i < tile.count * vecs; i += 64 * kLoraWaves) {
-      const int c = n_begin + i % vecs * 8;
-      const int64_t at = (int64_t)order[i / vecs] * a.N + c;
-      Raw8<T> r = {};
-      if (base != nullptr) r = load_raw(base + at, n_end - c);
-      store_row(y + at, n_end - c, r);
+    // 64 lanes a row of up to 512 channels, four rows of a wave under way
+    const int c = n_begin + lane * 8, left = n_end - c;
+    for (int t0 = 0; t0 < tile.count; t0 += 4 * kLoraWaves) {
+      Raw8<T> r[4] = {};
+      int64_t at[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = t0 + i * kLoraWaves + wave;
+        at[i] = (int64_t)order[t < tile.count ? t : t0] * a.N + c;
+        if (base != nullptr && t < tile.count) r[i] = load_raw(base + at[i], left);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t0 + i * kLoraWaves + wave < tile.count && left > 0) store_row(y + at[i], left, r[i]);
     }
     return;
   }
@@ -296,7 +304,7 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora_up(LoraArgs a) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int n = n0 + 8 * (row >> 2) + 4 * j + (row & 3);
-      const T* const br = b + (int64_t)(n < a.N ? n : a.N - 1) * a.rank;
+      const T* const br = b + (uint32_t)(n < a.N ? n : a.N - 1) * (uint32_t)a.rank;   // (below 2^28)
 #pragma unroll
       for (int k = 0; k < GN; ++k) {
         const int r = rank_at(chunk * GN + k);
@@ -457,7 +465,7 @@ static int run_lora(const LoraArgs& a, int64_t most, hipStream_t stream) {
   const size_t wide = lora_pitch(a.rank), lds = kLoraTile * (wide * 4 + (wide * 2 + 8) * 2);
   if (rb == 1) hipLaunchKernelGGL((k_lora_up<T, 1, 4>), up, block, lds, stream, a);
   else if (rb == 2) hipLaunchKernelGGL((k_lora_up<T, 2, 4>), up, block, lds, stream, a);
-  else hipLaunchKernelGGL((k_lora_up<T, 4, 3>), up, block, lds, stream, a);
+  else hipLaunchKernelGGL((k_lora_up<T, 4, 2>), up, block, lds, stream, a);
   return check_launch(what);
 }
 

@@ -216,6 +216,8 @@ template <typename T, int NV, int THR, bool TOKEN, bool BRANCH>
 static int launch_block(const BlockNormArgs& a, hipStream_t stream) {
   constexpr int RPB = THR == 64 ? 4 : 1, BLOCK = THR == 64 ? 256 : THR;
   const int64_t need = (a.rows + RPB - 1) / RPB;
+  // 16 waves per compute unit walk the rows (256 short-lived ones take the same time on streams from memory: 16384 x 4096 102
+  // us against 101, with a gate per token 129 / 127)
   const unsigned grid = grid_for(need * BLOCK, BLOCK, std::max(1, 16 * 64 / BLOCK));
   if constexpr (NV > 0)
     hipLaunchKernelGGL((k_block_norm<T, NV, THR, TOKEN, BRANCH>), dim3(grid), dim3(BLOCK), 0, stream, a);

@@ -7,7 +7,7 @@
 //   dw_post = sum over rows of e xh,   dgate = b dz xh w_post, summed over rows where they share it
 //
 // With a gate per channel both of its sums are one: P = sum over rows of dz xh, dw_post = b gate P and
-// dgate = b w_post P; with one per token the sum is of gate dz xh.  So every form has two sums per column.  Rows of 8 to 8192 elements are read
+// dgate = b w_post P; with one per token the sum is of gate dz xh.  So every form has two sums per column.  Rows of 8 to 8192 elements (of up to 16384 where there are not too many) are read
 // once: a grid of resident workgroups walks the rows, each thread keeps the sums of its own columns, and
 // the workgroups' sums are added by a second kernel in a fixed order (no atomics: the same
 // call gives the same bits).  dz stays in registers between the row's two reductions.
@@ -46,8 +46,10 @@ constexpr int kBlockWaves = 4;
 constexpr int kBlockHeld = 64;   // rows whose sums stay in registers before they join those of earlier rows
 
 // TOKEN: a gate per token and channel.  BRANCH: gradients of x, its norm and gate.  NORM: there is a dy.
-template <typename T, int NV, int THR, bool TOKEN, bool BRANCH, bool NORM>
+template <typename T, int NV, int THR, bool TOKEN, bool BRANCH, bool NORM, bool STREAM>
 __global__ __launch_bounds__(THR == 64 ? 64 * kBlockWaves : THR) void k_block_bwd(BlockNormBwdArgs a) {
+  // HELD: parameters, sums and the next row in registers; 1024 threads have 128 registers each, and keep their sums in LDS
+  constexpr bool HELD = THR < 1024;
   constexpr int RPB = THR == 64 ? kBlockWaves : 1, THREADS = RPB * THR, WAVES = THR / 64;
   __shared__ float lds[NV * 16 * THREADS + (THR == 64 ? 0 : 2 * 2 * WAVES)];
   float* const earlier = lds + threadIdx.x;
@@ -75,12 +77,12 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBlockWaves : THR) void k_block_bw
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if constexpr (NORM) {
-        o.dy[i] = load_row(dy + base, column(i), cols);
-        o.z[i] = load_row(z + base, column(i), cols);
+        o.dy[i] = load_row<STREAM>(dy + base, column(i), cols);
+        o.z[i] = load_row<STREAM>(z + base, column(i), cols);
       }
-      if (add != nullptr) o.add[i] = load_row(add + base, column(i), cols);
-      if constexpr (BRANCH) o.x[i] = load_row(x + base, column(i), cols);
-      if constexpr (TOKEN) o.g[i] = load_row(gate + base, column(i), cols);
+      if (add != nullptr) o.add[i] = load_row<STREAM>(add + base, column(i), cols);
+      if constexpr (BRANCH) o.x[i] = load_row<STREAM>(x + base, column(i), cols);
+      if constexpr (TOKEN) o.g[i] = load_row<STREAM>(gate + base, column(i), cols);
     }
     if constexpr (BRANCH) o.r1 = a.post_rstd[row];
     if constexpr (NORM) o.r2 = a.pre_rstd[row];
@@ -94,23 +96,56 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBlockWaves : THR) void k_block_bw
   };
   const int64_t step = (int64_t)gridDim.x * RPB, first = (int64_t)blockIdx.x * RPB + sub;
   Row next;
-  load(first < a.rows ? first : a.rows - 1, next);   // (a spare wave loads the last row)
+  if constexpr (HELD) load(first < a.rows ? first : a.rows - 1, next);   // (a spare wave loads the last row)
 
-  float w[BRANCH ? NV : 1][8], p[NORM ? NV : 1][8], s1[NV][8], s2[NV][8];
+  constexpr int HV = HELD ? NV : 1;
+  float held_w[HV][8], held_p[HV][8], s1[HV][8], s2[HV][8];
+  // what e w_post is of dz: b gate w_post, or b w_post with a gate per token
+  auto load_w = [&](int i, float w[8]) {
+    load_param8<T>(a.post, a.wf32, column(i), count(i), 1.0f, w);
+    float g[8];
+    load_param8<T>(TOKEN ? nullptr : a.gate, a.gate_f32, column(i), count(i), 1.0f, g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] *= a.b * g[j];
+  };
+  auto load_p = [&](int i, float p[8]) { load_param8<T>(a.pre, a.wf32, column(i), count(i), 1.0f, p); };
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    if constexpr (BRANCH) {
-      // what e w_post is of dz: b gate w_post, or b w_post with a gate per token
-      load_param8<T>(a.post, a.wf32, column(i), count(i), 1.0f, w[i]);
-      float g[8];
-      load_param8<T>(TOKEN ? nullptr : a.gate, a.gate_f32, column(i), count(i), 1.0f, g);
+    if constexpr (HELD) {
+      if constexpr (BRANCH) load_w(i, held_w[i]);
+      if constexpr (NORM) load_p(i, held_p[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[i][j] *= a.b * g[j];
+      for (int j = 0; j < 8; ++j) s1[i][j] = s2[i][j] = 0.0f;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) earlier[(i * 16 + j) * THREADS] = 0.0f;
     }
-    if constexpr (NORM) load_param8<T>(a.pre, a.wf32, column(i), count(i), 1.0f, p[i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s1[i][j] = s2[i][j] = 0.0f;
   }
+  auto weight = [&](int i, float w[8]) {
+    if constexpr (HELD) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = held_w[i][j];
+    } else {
+      load_w(i, w);
+    }
+  };
+  auto pre = [&](int i, float p[8]) {
+    if constexpr (HELD) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[j] = held_p[i][j];
+    } else {
+      load_p(i, p);
+    }
+  };
+  // adds x y to the first or second sum of column j of vector i
+  auto add1 = [&](int i, int j, float x, float y) {
+    if constexpr (HELD) s1[i][j] = __builtin_fmaf(x, y, s1[i][j]);
+    else earlier[(i * 16 + j) * THREADS] = __builtin_fmaf(x, y, earlier[(i * 16 + j) * THREADS]);
+  };
+  auto add2 = [&](int i, int j, float x, float y) {
+    if constexpr (HELD) s2[i][j] = __builtin_fmaf(x, y, s2[i][j]);
+    else earlier[(i * 16 + 8 + j) * THREADS] = __builtin_fmaf(x, y, earlier[(i * 16 + 8 + j) * THREADS]);
+  };
 
   // A cut vector is read as its row's last 8 elements, which another wave may write in place: of the
   // first row all are read before any is written (of later rows the reductions' barriers see to it).
@@ -118,58 +153,61 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBlockWaves : THR) void k_block_bw
   int turn = 0;
   bool more = false;   // there are sums of earlier rows
   for (int64_t row = first;;) {
-    const int64_t stop = std::min(row + kBlockHeld * step, a.rows);
+    const int64_t stop = HELD ? std::min(row + kBlockHeld * step, a.rows) : a.rows;
     for (; row < stop; row += step, turn ^= 1) {
       float* const sc = scratch + (THR > 64 ? turn * 2 * WAVES : 0);
       const int64_t base = row * cols;
+      if constexpr (!HELD) load(row, next);
       const Row now = next;
-      load(row + step < a.rows ? row + step : row, next);
+      if constexpr (HELD) load(row + step < a.rows ? row + step : row, next);
       float mean = 0.0f, dz[NV][8];
       if constexpr (NORM) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          float vd[8], zh[8];
+          float vd[8], zh[8], p[8];
           widen(now.dy[i], i, vd);
           widen(now.z[i], i, zh);
+          pre(i, p);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             zh[j] *= now.r2;
-            mean = __builtin_fmaf(vd[j] * p[i][j], zh[j], mean);
-            s2[i][j] = __builtin_fmaf(vd[j], zh[j], s2[i][j]);
+            mean = __builtin_fmaf(vd[j] * p[j], zh[j], mean);
+            add2(i, j, vd[j], zh[j]);
           }
         }
         mean = row_sum<THR>(mean, sc) * inv_cols;
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        float vd[8] = {}, zh[8] = {}, va[8] = {}, none[8] = {};
+        float vd[8] = {}, zh[8] = {}, va[8] = {}, p[8] = {};
         if constexpr (NORM) {
+          pre(i, p);
           widen(now.dy[i], i, vd);
           widen(now.z[i], i, zh);
 #pragma unroll
           for (int j = 0; j < 8; ++j) zh[j] *= now.r2;
         }
         if (add != nullptr) widen(now.add[i], i, va);
-        block_dz<T>(a, base + column(i), count(i), vd, zh, NORM ? p[i] : none, va, NORM ? now.r2 : 0.0f,
-                    mean, dz[i]);
+        block_dz<T>(a, base + column(i), count(i), vd, zh, p, va, NORM ? now.r2 : 0.0f, mean, dz[i]);
       }
       if constexpr (BRANCH) {
         mean = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           if (i == NV - 1) mask.clear(dz[i]);   // (0 times a row's infinity)
-          float xh[8], g[8], dg[8];
+          float xh[8], g[8], dg[8], w[8];
+          weight(i, w);
           widen(now.x[i], i, xh);
           if constexpr (TOKEN) widen(now.g[i], i, g);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             xh[j] *= now.r1;
             if constexpr (TOKEN) {
-              dg[j] = dz[i][j] * w[i][j] * xh[j];
+              dg[j] = dz[i][j] * w[j] * xh[j];
               dz[i][j] *= g[j];
             }
-            s1[i][j] = __builtin_fmaf(dz[i][j], xh[j], s1[i][j]);
-            dz[i][j] *= w[i][j];
+            add1(i, j, dz[i][j], xh[j]);
+            dz[i][j] *= w[j];
             mean = __builtin_fmaf(dz[i][j], xh[j], mean);
           }
           if constexpr (TOKEN)
@@ -190,26 +228,30 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBlockWaves : THR) void k_block_bw
       }
     }
     if (row >= a.rows) break;
+    if constexpr (HELD) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float *const e1 = earlier + (i * 16 + j) * THREADS, *const e2 = e1 + 8 * THREADS;
-        *e1 = more ? *e1 + s1[i][j] : s1[i][j];
-        *e2 = more ? *e2 + s2[i][j] : s2[i][j];
-        s1[i][j] = s2[i][j] = 0.0f;
-      }
-    more = true;
+        for (int j = 0; j < 8; ++j) {
+          float *const e1 = earlier + (i * 16 + j) * THREADS, *const e2 = e1 + 8 * THREADS;
+          *e1 = more ? *e1 + s1[i][j] : s1[i][j];
+          *e2 = more ? *e2 + s2[i][j] : s2[i][j];
+          s1[i][j] = s2[i][j] = 0.0f;
+        }
+      more = true;
+    }
   }
   if (!a.sums) return;
-  if (more) {
+  if constexpr (HELD) {
+    if (more) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        s1[i][j] += earlier[(i * 16 + j) * THREADS];
-        s2[i][j] += earlier[(i * 16 + 8 + j) * THREADS];
-      }
+        for (int j = 0; j < 8; ++j) {
+          s1[i][j] += earlier[(i * 16 + j) * THREADS];
+          s2[i][j] += earlier[(i * 16 + 8 + j) * THREADS];
+        }
+    }
   }
   if constexpr (THR == 64) {
     // the waves' sums, halved in two steps through LDS (lane-major: no conflicts)
@@ -244,8 +286,14 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBlockWaves : THR) void k_block_bw
 #pragma unroll
   for (int i = 0; i < NV; ++i)
     if (count(i) > 0) {
-      store8(out + column(i), count(i), s1[i]);
-      store8(out + cols + column(i), count(i), s2[i]);
+      float v1[8], v2[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v1[j] = HELD ? s1[HELD ? i : 0][j] : earlier[(i * 16 + j) * THREADS];
+        v2[j] = HELD ? s2[HELD ? i : 0][j] : earlier[(i * 16 + 8 + j) * THREADS];
+      }
+      store8(out + column(i), count(i), v1);
+      store8(out + cols + column(i), count(i), v2);
     }
 }
 
@@ -415,24 +463,34 @@ static int launch_block_parts(const BlockPartsArgs& p, hipStream_t stream) {
   return check_launch("block_norm_backward");
 }
 
-template <typename T, int NV, int THR, bool TOKEN, bool BRANCH, bool NORM>
-static int launch_block_bwd(const BlockNormBwdArgs& a, BlockPartsArgs p, hipStream_t stream) {
+template <typename T, int NV, int THR, bool TOKEN, bool BRANCH, bool NORM, bool STREAM>
+static int launch_block_bwd_as(const BlockNormBwdArgs& a, BlockPartsArgs p, hipStream_t stream) {
   constexpr int RPB = THR == 64 ? kBlockWaves : 1;
   static const int resident = [] {
     int n = 0;
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, (k_block_bwd<T, NV, THR, TOKEN, BRANCH, NORM>),
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, (k_block_bwd<T, NV, THR, TOKEN, BRANCH, NORM, STREAM>),
                                                      RPB * THR, 0) != hipSuccess || n < 1)
       n = 1;
     return std::min(n, std::max(1, 16 * 64 / (NV * RPB * THR)));
   }();
   const int64_t cap = std::min<int64_t>(FP8DP_NORM_PARTS, (int64_t)num_cus() * resident);
   const int64_t grid = std::min<int64_t>((a.rows + RPB - 1) / RPB, cap);
-  hipLaunchKernelGGL((k_block_bwd<T, NV, THR, TOKEN, BRANCH, NORM>), dim3((unsigned)grid), dim3(RPB * THR), 0,
+  hipLaunchKernelGGL((k_block_bwd<T, NV, THR, TOKEN, BRANCH, NORM, STREAM>), dim3((unsigned)grid), dim3(RPB * THR), 0,
                      stream, a);
   const int rc = check_launch("block_norm_backward");
   if (rc || !a.sums) return rc;
   p.nparts = (int)grid;
   return launch_block_parts<T>(p, stream);
+}
+
+// Beyond the 256 MB of the last-level cache: read past the caches.
+template <typename T, int NV, int THR, bool TOKEN, bool BRANCH, bool NORM>
+static int launch_block_bwd(const BlockNormBwdArgs& a, const BlockPartsArgs& p, hipStream_t stream) {
+  const int64_t tensors = 1 + 2 * NORM + (a.dz_add != nullptr) + (BRANCH ? 1 + (a.dx != nullptr) : 0) +
+                          (TOKEN ? 1 + (a.dgate != nullptr) : 0);
+  if (a.rows * a.cols * tensors * (int64_t)sizeof(T) > ((int64_t)256 << 20))
+    return launch_block_bwd_as<T, NV, THR, TOKEN, BRANCH, NORM, true>(a, p, stream);
+  return launch_block_bwd_as<T, NV, THR, TOKEN, BRANCH, NORM, false>(a, p, stream);
 }
 
 template <typename T, bool TOKEN, bool BRANCH, bool NORM>
@@ -444,6 +502,9 @@ static int launch_block_width(const BlockNormBwdArgs& a, BlockPartsArgs p, hipSt
     if (nvec <= 256) return launch_block_bwd<T, 1, 256, TOKEN, BRANCH, NORM>(a, p, stream);
     if (nvec <= 512) return launch_block_bwd<T, 2, 256, TOKEN, BRANCH, NORM>(a, p, stream);
     if (nvec <= 1024) return launch_block_bwd<T, 2, 512, TOKEN, BRANCH, NORM>(a, p, stream);
+    // sums of up to 64 rows each, one after another (2048 x 16384: 558 us by the kernel below)
+    if (nvec <= 2048 && a.rows <= 64 * (int64_t)num_cus())
+      return launch_block_bwd<T, 2, 1024, TOKEN, BRANCH, NORM>(a, p, stream);
   }
   // below FP8DP_NORM_PARTS rows each has a workgroup; of more, half the parts are sums and half what they lost
   const bool one = a.rows < FP8DP_NORM_PARTS;

@@ -40,7 +40,7 @@ typedef enum {
 #define FP8DP_GATED_MAX_ROWS 16777216
 
 /* Bytes of workspace with which gated_linear splits K over workgroups where there are few
-   tiles of h; 0 where it would not. */
+   tiles of h, and copies operands whose rows K cuts to aligned ones; 0 where it would do neither. */
 int64_t gated_linear_workspace(int64_t M, int64_t N, int64_t K);
 
 /* The first half of a gated feed-forward layer, in one kernel:
@@ -48,10 +48,10 @@ int64_t gated_linear_workspace(int64_t M, int64_t N, int64_t K);
    x: [M x K], w_gate, w_up: [N x K], h: [M x N], all of type dt, FP8DP_BF16 or FP8DP_F16.
    gate, up: [M x N] of type dt, g and u rounded, for the backward pass; both or neither.
    workspace: 16-byte aligned scratch, or NULL; with less than gated_linear_workspace()
-   bytes K is not split.
+   bytes K is not split and nothing copied.
    Errors: EINVAL for a NULL x, w_gate, w_up or h, one of gate and up without the other, M
    outside 1 .. FP8DP_GATED_MAX_ROWS, N or K outside 1 .. FP8DP_GATED_MAX_WIDTH, another type, an unknown
-   act, a misaligned pointer, or workspace_bytes < 0. */
+   act, a misaligned pointer, an output that is an input or another output, or workspace_bytes < 0. */
 int gated_linear(const void* x, const void* w_gate, const void* w_up, int64_t M, int64_t N,
                  int64_t K, fp8dp_dtype dt, fp8dp_gate act, void* h, void* gate, void* up,
                  void* workspace, int64_t workspace_bytes, hipStream_t stream);
@@ -89,7 +89,7 @@ int gated_linear_backward(const void* dh, const void* gate, const void* up, cons
    where the formula does; other rows are not touched by it.
    Errors: EINVAL for a NULL residual, z without x or x without z, neither z nor y, what belongs to
    an x that is NULL, rows or cols out of layer_norm's range, unknown types, a misaligned pointer, an eps that is
-   negative or not finite, a scale that is not finite, or y the same buffer as z or the normed residual. */
+   negative or not finite, a scale that is not finite, or y the same buffer as z or an input. */
 int block_norm(const void* x, const void* residual, const void* post_weight, const void* gate,
                int32_t gate_per_token, const void* pre_weight, int64_t rows, int64_t cols,
                fp8dp_dtype dt, fp8dp_dtype wt, fp8dp_dtype gt, float residual_scale,

@@ -825,7 +825,8 @@ def _bytes(t) -> int:
 
 
 def gated_linear_workspace(M: int, N: int, K: int) -> int:
-    """Bytes of workspace with which gated_linear splits K where there are few tiles; may be 0."""
+    """Bytes of workspace with which gated_linear splits K where there are few tiles, and copies
+    operands whose rows K cuts; may be 0."""
     return lib().gated_linear_workspace(M, N, K)
 
 
@@ -850,7 +851,7 @@ def gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act:
     """h [..., N] = f(x w_gate^T) * (x w_up^T) for x [..., K] and weights [N, K], bfloat16 or
     float16; act: GATE_SILU, ...; gate, up: the two products, for the backward pass.  workspace
     (any contiguous tensor of gated_linear_workspace bytes, 16-byte aligned) lets K be split
-    where h is small."""
+    where h is small, and operands with cut rows be copied."""
     M, N, K, dt = _gated("gated_linear", x, w_gate, w_up, (("h", h), ("gate", gate), ("up", up)))
     room = _bytes(workspace)
     x, w_gate, w_up, h, gate, up, workspace, s = _args(stream, x, w_gate, w_up, h, gate, up, workspace)

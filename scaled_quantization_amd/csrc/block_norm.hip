@@ -284,8 +284,8 @@ extern "C" int block_norm(const void* x, const void* residual, const void* post_
       !aligned_to(post_weight, we) || !aligned_to(pre_weight, we) ||
       !aligned_to(gate, dtype_size(gt)) || !aligned_to(post_rstd, 4) || !aligned_to(pre_rstd, 4))
     return bad_align(what);
-  if (y != nullptr && (y == z || (x == nullptr && y == residual))) {
-    set_error("%s: y must not be z, nor the residual that is normed", what);
+  if (y != nullptr && (y == z || y == x || y == residual || (token && y == gate))) {
+    set_error("%s: y must not be z, nor an input", what);
     return FP8DP_EINVAL;
   }
   BlockNormArgs a = {};

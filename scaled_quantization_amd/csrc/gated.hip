@@ -102,7 +102,10 @@ __global__ __launch_bounds__(256) void k_gated_join(const float* parts, int spli
 // weight's rows as its first operand, so a lane ends with one token and four channels.  Rows may start and
 // end at any byte: a chunk that K cuts is read as the row's last 8 values and shifted.
 constexpr int kFewWaves = 8, kFewTokens16 = 64;
-constexpr int64_t kRingWork = (int64_t)256 * 1024;   // groups of 16 channels x K from which on rings are used
+// Groups of 16 channels x K from which on rings are used.  Rings / straight from memory (us): 1 x 4096 x 4096 13.4 / 14.1,
+// 1 x 16384 x 4096 47.8 / 51.9, 16 x 1024 x 4096 8.8 / 13.1, 64 x 16384 x 4096 63.6 / 101.7; below, one stage of K or two a wave
+// fill no ring.
+constexpr int64_t kRingWork = (int64_t)256 * 1024;
 
 template <typename T>
 __device__ __forceinline__ v8s_t as_frag(const Raw8<T>& r) {
@@ -193,7 +196,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(const T* x, const 
 
 // The same for rows that start at multiples of 16 bytes.  Fragments read straight from memory have 16 rows in consecutive
 // lanes, which the compute unit takes one 16-byte piece a cycle; here each wave copies whole cache lines into a ring of its
-// own in LDS, 8 rows x 128 bytes a copy, four times the rate (48 tokens x 16384 x 4096: 85 -> 47 us).  Stages of 64 k go to the waves
+// own in LDS, 8 rows x 128 bytes a copy, four times the rate (48 tokens x 16384 x 4096: 85 -> 59 us).  Stages of 64 k go to the waves
 // in turn; the grid is resident, and a wave's ring runs on into the workgroup's next 16 channels while their sums
 // are joined.  W waves and S slots: 64 KiB or more under way in each compute unit.
 template <typename T, int MT, int W, int S>
@@ -425,10 +428,13 @@ extern "C" int gated_linear(const void* x, const void* w_gate, const void* w_up,
   if (!aligned_to(x, 2) || !aligned_to(w_gate, 2) || !aligned_to(w_up, 2) || !aligned_to(h, 2) ||
       !aligned_to(gate, 2) || !aligned_to(up, 2))
     return bad_align(what);
-  if (h == gate || h == up || (gate != nullptr && gate == up)) {
-    set_error("%s: h, gate and up must be different buffers", what);
-    return FP8DP_EINVAL;
-  }
+  const void* const all[] = {x, w_gate, w_up, h, gate, up};
+  for (int i = 3; i < 6; ++i)
+    for (int j = 0; j < i; ++j)
+      if (all[i] != nullptr && all[i] == all[j]) {
+        set_error("%s: h, gate and up must be different buffers, and no inputs", what);
+        return FP8DP_EINVAL;
+      }
   auto run = [&](auto t) {
     using T = decltype(t);
     return run_gated<T>(what, static_cast<const T*>(x), static_cast<const T*>(w_gate),

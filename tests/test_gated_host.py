@@ -127,6 +127,8 @@ def test_c_refusals(L):
     refused(gl(u=48), b"together")
     refused(gl(g=32, u=48), b"different")
     refused(gl(g=48, u=48), b"different")
+    refused(gl(h=16), b"different")
+    refused(gl(g=16, u=48), b"different")
     refused(gl(x=17), b"aligned")
     refused(gl(g=49, u=64), b"aligned")
     refused(gl(ws=24, room=64), b"workspace")
@@ -166,6 +168,8 @@ def test_c_refusals(L):
     for kw in ({"x": 17}, {"z": 33}, {"gate": 17}, {"gate": 18, "gt": 2}, {"r1": 18}):
         refused(bn(**kw), b"aligned")
     refused(bn(z=64), b"must not be")
+    refused(bn(y=16), b"must not be")
+    refused(bn(y=16, x=96, gate=16, tok=1, res=112), b"must not be")
     refused(bn(x=None, z=None, post=None, gate=None, y=16), b"must not be")
     # block_norm_backward(dy, add, x, z, post, gate, per_token, pre, r1, r2, rows, cols, dt, wt, gt, a, b, dres, dx,
     #                     dgate, dpost, dpre, ws, stream)

@@ -142,7 +142,8 @@ int64_t lora_add_workspace(int64_t tokens, int64_t N, int64_t K, int64_t rank, i
 /* Adds the low-rank products of the tokens' adapters to the output of a shared projection:
      y[t] = base[t] + scale[i] * b_i (a_i x[t]) with i = index[t]; y[t] = base[t] without an adapter.
    x: [tokens x K], a: [adapters x rank x K], b: [adapters x N x rank], base, y: [tokens x N], all of
-   type dt, FP8DP_BF16 or FP8DP_F16; scale: [adapters] floats; the products a_i x[t] are held in binary32.
+   type dt, FP8DP_BF16 or FP8DP_F16; scale: [adapters] floats; the products a_i x[t] are summed in
+   binary32 and multiplied by b_i as two 16-bit parts each, 16 bits of them in bfloat16 and 22 in float16.
    ranks: [adapters] 32-bit integers, of adapter i the first ranks[i] rows of a and columns of b count
    (what the others hold does not matter; below 0 is 0, above rank is rank), or NULL: all.
    plan: lora_plan's for the same tokens and adapters.  base NULL: zeros.  y may be base.

@@ -8,8 +8,13 @@
 // D is in the workspace: rows of 2 Np values, Np = N to a multiple of 64, and as many rows as M to a
 // multiple of 64; what pads it is zeros, so that every stage of K is whole on D's side.  Rounding
 // dg and du to 16 bits, as the matrix instructions take them, is off by half a step of the type per term;
-// the products sum them in binary32.
+// the products sum them in binary32.  (One pass forms dg and du for both products: formed
+// in the products' loads they would be computed once per tile of K, 4 times each at the size below.)
+//
+// 16384 x 2048 x 768: the pass over dh, gate and up 50 us (6.7 TB/s), dx 104, the weights' 105 and 10 for their join: 206
+// GFLOP in two products, 0.99 PFLOP/s, whose waves wait for their operands half of the time.
 #include "gated_core.hpp"
+#include "pad16.hpp"
 
 namespace fp8dp {
 

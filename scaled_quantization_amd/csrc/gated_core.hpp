@@ -53,7 +53,8 @@ __device__ __forceinline__ float gate_of(float g, float* slope) {
 }
 
 // f(std::integral_constant<int, act>): one branch for a whole tile or kernel.  (A branch per element made 64 times seven
-// pieces of code of a tile's outputs, which the instruction cache does not hold: 7 us per tile of 256 x 256.)
+// pieces of code of a tile's outputs, which the instruction cache does not hold: 16384 x 8192 x 128, 180 us
+// against 126.)
 template <typename F>
 __device__ __forceinline__ void with_act(int act, F&& f) {
   switch (act) {
@@ -106,6 +107,13 @@ inline int64_t tiles_of(TileShape t, int64_t m, int64_t n) {
   const int64_t bn = t == kTile256 ? 256 : t == kTile192 ? 192 : 128;
   return ((m + bm - 1) / bm) * ((n + bn - 1) / bn);
 }
+// The plan of the least estimate, in us: a workgroup's stages of 64 of K and, for each tile, its ends (the first copies,
+// the outputs).  The stages' times were measured, as the difference of K = 4096 and 1024 over 48, with every compute unit busy
+// with one tile or two: 256 x 256 1.40 .. 1.72 (4096 x 4096), 256 x 192 1.02 .. 1.04, 128 x 128 0.44 .. 0.49 where it has a
+// compute unit to itself, 0.80 .. 0.85 for two, at any alignment 1.04 .. 1.30 and 1.35 .. 1.56.  A K that is
+// shared costs a join.  With estimates that favoured shares by a third more, gradients of 1025 x 1023 x 1001 took 50.5 us
+// for 45.9 (dx from three shares, now one), 8192 x 2048 x 768 169 for 161, one forward of 100 x 1024 x 1024 14.1 for 11.6;
+// 1000 x 8192 x 4096 is the worst loss that was found (302, now 312).
 inline ProductPlan plan_product(int64_t m, int64_t n, int64_t stages, bool dual, bool direct) {
   const double cus = num_cus();
   ProductPlan best = {direct ? kTile256 : kTileAny, 1};
@@ -124,55 +132,15 @@ inline ProductPlan plan_product(int64_t m, int64_t n, int64_t stages, bool dual,
     }
   };
   if (direct) {
-    offer(kTile256, 1.6, 1.6, 1, 4.0);
-    if (!dual) offer(kTile192, 1.25, 1.25, 1, 3.5);
-    offer(kTile128, 0.95, 0.65, 2, 3.0);
+    offer(kTile256, 1.45, 1.45, 1, 5.0);
+    if (!dual) offer(kTile192, 1.05, 1.05, 1, 4.5);
+    offer(kTile128, 0.82, 0.45, 2, 3.5);
   } else {
-    offer(kTileAny, 1.5, 0.8, 2, 3.0);
+    offer(kTileAny, 1.45, 1.15, 2, 3.5);
   }
   return best;
 }
 
 inline int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
-
-// Copies with aligned rows of up to three matrices of `cols` columns, zeros behind them, in one launch: rows of a K that
-// is no multiple of 8 start anywhere, and the tiles that are filled by copies are then worth more than the copies cost.
-struct PadArgs {
-  const uint16_t* from[3];
-  uint16_t* to[3];
-  int64_t rows[3];   // ends of the three, in rows of all
-  int cols, ld;
-};
-static __global__ __launch_bounds__(256) void k_pad16(PadArgs a) {
-  const uint32_t nvec = (uint32_t)a.ld / 8;
-  const uint64_t total = (uint64_t)a.rows[2] * nvec, step = (uint64_t)gridDim.x * 256;
-  for (uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += step) {
-    const int64_t row = total >> 32 ? at / nvec : (uint32_t)at / nvec;
-    const int c = (int)(at - (uint64_t)row * nvec) * 8, which = (row >= a.rows[0]) + (row >= a.rows[1]);
-    const int64_t r = row - (which == 0 ? 0 : which == 1 ? a.rows[0] : a.rows[1]);
-    const uint16_t* const from = which == 0 ? a.from[0] : which == 1 ? a.from[1] : a.from[2];
-    uint16_t* const to = which == 0 ? a.to[0] : which == 1 ? a.to[1] : a.to[2];
-    const Raw8<bf16_t> v = load_raw(reinterpret_cast<const bf16_t*>(from) + r * a.cols + c, a.cols - c);
-    *reinterpret_cast<u32x4_t*>(to + r * a.ld + c) = u32x4_t{v.w[0], v.w[1], v.w[2], v.w[3]};
-  }
-}
-// x [M x cols], w0 and w1 [N x cols] to `to`, one behind the other; pad_bytes() of them.
-inline int64_t pad_ld(int64_t cols) { return round_up(cols, 8); }
-inline int64_t pad_bytes(int64_t M, int64_t N, int64_t cols) {
-  return round_up((M + 2 * N) * pad_ld(cols) * 2, 256);
-}
-inline int pad_operands(const char* what, const uint16_t* x, const uint16_t* w0, const uint16_t* w1, int64_t M,
-                        int64_t N, int64_t cols, uint16_t* to, hipStream_t stream) {
-  const int64_t ld = pad_ld(cols);
-  const PadArgs a = {{x, w0, w1}, {to, to + M * ld, to + (M + N) * ld}, {M, M + N, M + 2 * N}, (int)cols, (int)ld};
-  hipLaunchKernelGGL(k_pad16, dim3(grid_for((M + 2 * N) * (ld / 8), 256, 32)), dim3(256), 0, stream, a);
-  return check_launch(what);
-}
-// Whether the copies pay for themselves, by M N K (measured, copied / as they are, us): forward 777 x 1023 x 1001 21.2 /
-// 25.8, 777 x 1023 x 101 10.9 / 9.5, 300 x 600 x 301 12.5 / 11.7; backward, where two products share
-// them, 777 x 1023 x 1001 46.8 / 58.1, 777 x 1023 x 101 39.8 / 44.5, 100 x 300 x 1001 25.7 / 30.9, 300 x 300 x 301 28.9 / 35.2.
-inline bool pad_pays(int64_t M, int64_t N, int64_t K, bool backward) {
-  return K % 8 != 0 && (double)M * (double)N * (double)K >= (backward ? 8e6 : 256e6);
-}
 
 }  // namespace fp8dp

@@ -5,7 +5,10 @@
 // A plan, made once per step, orders the tokens by adapter and cuts each adapter's into tiles of up to
 // 32, so that an adapter's weights are read once per tile.  Two kernels follow: the first gathers a
 // tile's tokens and leaves v in binary32, K split over workgroups where there are few tiles; the second adds
-// the ranges up and multiplies by b.  v goes to the matrix instructions as a sum of two 16-bit
+// the ranges up and multiplies by b.  Each reads its weights once a tile; what bounds both is the way from the plan to the
+// data (entry, order, rows, weights: one waits for the other), so as many workgroups as fit are under way and each loads
+// ahead.  64 tokens of 64 adapters, ranks of 16, 4096 x 4096: 4.7 and 7.5 us; 5003 tokens of 8, ranks of 64: 19 and 42 us,
+// where 131 MB at the rate of a large copy would be 20 in all.  v goes to the matrix instructions as a sum of two 16-bit
 // values, scaled by a power of two per token: of up to 16 ranks, which fill half of an instruction's 32, the low parts
 // take the other half; more have an instruction for each part.
 #include "gated_core.hpp"
@@ -230,18 +233,13 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
   }
 }
 
-// 8 outputs that stay in the caches: 64 bytes of a row are half a cache line, whose other half another wave stores, and
-// past the caches each half is a write of its own.
-template <typename T>
-__device__ __forceinline__ void store_kept(T* p, int n, const float v[8]) {
-  if (n >= 8) *reinterpret_cast<u32x4_e_t*>(p) = round8(v, T{}).w;
-  else store8(p, n, v);
-}
-
 // y of a tile.  A wave takes 32 channels a step; pairs of instructions give a lane one token and 8 consecutive
 // channels.  What a step reads (base and b, up to 16 RB ranks) is loaded DEPTH steps ahead, the first of them
-// before v is there.  v is staged in LDS as 16-bit pairs [token][GR ranks: GR high parts, GR low parts].
-constexpr int kLoraChannels = 512;   // of a workgroup (64 lanes x 8)
+// before v is there (of 64 ranks two steps: a third no longer fits the registers of four waves, 51 us for 42 with 5003
+// tokens).  v is staged in LDS as 16-bit pairs [token][GR ranks: GR high parts, GR low parts].
+// Channels of a workgroup, 64 lanes x 8.  (1024, which stage v half as often, take 10.9 us for 7.1 with 64 tokens and 49.5
+// for 50.7 with 5003, both measured before the tokens without an adapter went four rows at a time.)
+constexpr int kLoraChannels = 512;
 constexpr int kLoraSplits = 8;       // most ranges of K
 template <typename T, int RB, int DEPTH>
 __global__ __launch_bounds__(64 * kLoraWaves, 4) void k_lora_up(LoraArgs a) {
@@ -425,7 +423,7 @@ __global__ __launch_bounds__(64 * kLoraWaves, 4) void k_lora_up(LoraArgs a) {
       widen8f(old[i], was);
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[j] = __builtin_fmaf(acc[i][j >> 2][j & 3], f, was[j]);
-      store_kept(y + token[i] + c, left, sum);
+      store8(y + token[i] + c, left, sum);
     }
   };
   for (int s = 0; s < steps; s += DEPTH) {
@@ -438,7 +436,8 @@ __global__ __launch_bounds__(64 * kLoraWaves, 4) void k_lora_up(LoraArgs a) {
   }
 }
 
-// Over how many ranges K is split: a workgroup for every compute unit, ranges of 512 or more.
+// Over how many ranges K is split: four workgroups for every compute unit, each of 512 or more of K (a step of its eight
+// waves); more ranges are more to add up for every workgroup of the second kernel.
 struct LoraSplit {
   int splits, range;
 };

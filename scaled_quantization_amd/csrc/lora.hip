@@ -7,7 +7,7 @@
 // tile's tokens and leaves v in binary32, K split over workgroups where there are few tiles; the second adds
 // the ranges up and multiplies by b.  Each reads its weights once a tile; what bounds both is the way from the plan to the
 // data (entry, order, rows, weights: one waits for the other), so as many workgroups as fit are under way and each loads
-// ahead.  64 tokens of 64 adapters, ranks of 16, 4096 x 4096: 4.7 and 7.5 us; 5003 tokens of 8, ranks of 64: 19 and 42 us,
+// ahead.  64 tokens of 64 adapters, ranks of 16, 4096 x 4096: 4.7 and 8 us; 5003 tokens of 8, ranks of 64: 16 and 36 us,
 // where 131 MB at the rate of a large copy would be 20 in all.  v goes to the matrix instructions as a sum of two 16-bit
 // values, scaled by a power of two per token: of up to 16 ranks, which fill half of an instruction's 32, the low parts
 // take the other half; more have an instruction for each part.
@@ -146,7 +146,7 @@ struct LoraArgs {
   const void *x, *a, *b, *base;
   const float* scale;
   const int32_t* ranks;
-  int N, K, rank, adapters, splits, k_range;
+  int N, K, rank, adapters, splits, k_range, most;   // most: tiles that the plan has room for
   void* y;
   float* v;   // [split][place][lora_pitch(rank)]
 };
@@ -168,8 +168,9 @@ template <typename T, int RB>
 __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
   __shared__ v4f_t sums[kDownWaves][RB][2][64];
   LoraTile tile;
-  if (!lora_tile(a.plan, a.adapters, blockIdx.x, &tile) || tile.adapter < 0) return;
-  const int rank = lora_rank(a, tile.adapter), r0 = blockIdx.z * 16 * RB;
+  const uint32_t at_tile = blockIdx.x / (uint32_t)a.splits, split = blockIdx.x - at_tile * (uint32_t)a.splits;
+  if (!lora_tile(a.plan, a.adapters, (int)at_tile, &tile) || tile.adapter < 0) return;
+  const int rank = lora_rank(a, tile.adapter), r0 = blockIdx.y * 16 * RB;
   if (r0 >= rank) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, part = lane >> 4;
@@ -189,7 +190,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
   v4f_t acc[RB][2];
 #pragma unroll
   for (int b = 0; b < RB; ++b) acc[b][0] = acc[b][1] = v4f_t{0.0f, 0.0f, 0.0f, 0.0f};
-  const int begin = blockIdx.y * a.k_range, end = begin + a.k_range < a.K ? begin + a.k_range : a.K;
+  const int begin = (int)split * a.k_range, end = begin + a.k_range < a.K ? begin + a.k_range : a.K;
   auto block = [&](int k0, auto WHOLE) {
     constexpr bool whole = decltype(WHOLE)::value;
     Raw8<T> w[RB][2], x[2][2];
@@ -229,7 +230,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
     v4f_t s = sums[0][b][half][l];
 #pragma unroll
     for (int w = 1; w < kDownWaves; ++w) s += sums[w][b][half][l];
-    *reinterpret_cast<v4f_t*>(a.v + ((int64_t)blockIdx.y * a.plan.tokens + tile.start + token) * rp + r) = s;
+    *reinterpret_cast<v4f_t*>(a.v + ((int64_t)split * a.plan.tokens + tile.start + token) * rp + r) = s;
   }
 }
 
@@ -237,20 +238,24 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
 // channels.  What a step reads (base and b, up to 16 RB ranks) is loaded DEPTH steps ahead, the first of them
 // before v is there (of 64 ranks two steps: a third no longer fits the registers of four waves, 51 us for 42 with 5003
 // tokens).  v is staged in LDS as 16-bit pairs [token][GR ranks: GR high parts, GR low parts].
-// Channels of a workgroup, 64 lanes x 8.  (1024, which stage v half as often, take 10.9 us for 7.1 with 64 tokens and 49.5
-// for 50.7 with 5003, both measured before the tokens without an adapter went four rows at a time.)
+// Channels of a workgroup, 64 lanes x 8.  (1024, which stage v half as often: 16 us for 13 with 64 tokens and 57 for 53
+// with 5003, both kernels.)  A wave's are in a row: the halves of a cache line are read, and stored, one after the other by
+// the same wave.  The workgroups of a tile follow each other, so that whole rows are under way (both together: 20000
+// tokens 170 us, now 157).
 constexpr int kLoraChannels = 512;
 constexpr int kLoraSplits = 8;       // most ranges of K
+constexpr int kLoraGridY = 32768;    // tiles of the grid's second dimension
 template <typename T, int RB, int DEPTH>
 __global__ __launch_bounds__(64 * kLoraWaves, 4) void k_lora_up(LoraArgs a) {
   constexpr int GR = RB == 1 ? 16 : 32, GN = RB == 1 ? 1 : RB / 2;   // ranks of a group, groups of a chunk
   extern __shared__ __attribute__((aligned(16))) uint8_t shared_up[];
   __shared__ float factor[kLoraTile];
   LoraTile tile;
-  if (!lora_tile(a.plan, a.adapters, blockIdx.x, &tile)) return;
+  const int at_tile = blockIdx.y + blockIdx.z * kLoraGridY;
+  if (at_tile >= a.most || !lora_tile(a.plan, a.adapters, at_tile, &tile)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rank = tile.adapter < 0 ? 0 : lora_rank(a, tile.adapter);
-  const int n_begin = blockIdx.y * kLoraChannels, n_end = std::min<int>(a.N, n_begin + kLoraChannels);
+  const int n_begin = blockIdx.x * kLoraChannels, n_end = std::min<int>(a.N, n_begin + kLoraChannels);
   const int32_t* const order = a.plan.order() + tile.start;
   const T* const base = static_cast<const T*>(a.base);
   T* const y = static_cast<T*>(a.y);
@@ -288,11 +293,12 @@ __global__ __launch_bounds__(64 * kLoraWaves, 4) void k_lora_up(LoraArgs a) {
   struct Step {
     Raw8<T> old[2], w[GN][2];
   };
-  const int turns = (n_end - n_begin - wave * 32 + kLoraWaves * 32 - 1) / (kLoraWaves * 32), steps = turns * chunks;
+  const int per = (n_end - n_begin + kLoraWaves * 32 - 1) / (kLoraWaves * 32) * 32, first = n_begin + wave * per;
+  const int turns = first < n_end ? (std::min(n_end - first, per) + 31) / 32 : 0, steps = turns * chunks;
   auto load = [&](int s, Step& o) {
     if (s >= steps) return;
     const int turn = chunks == 1 ? s : s / chunks, chunk = s - turn * chunks;
-    const int n0 = n_begin + (turn * kLoraWaves + wave) * 32, c = n0 + 8 * part;
+    const int n0 = first + turn * 32, c = n0 + 8 * part;
     if (chunk == 0 && base != nullptr) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -318,10 +324,10 @@ __global__ __launch_bounds__(64 * kLoraWaves, 4) void k_lora_up(LoraArgs a) {
     load(d, ahead[d]);
   }
 
-  // v: the ranges' sums in binary32, then the pairs (8 threads a token)
+  // v: the ranges' sums in binary32 (rows of 8 words more: 8 tokens are read at once), then the pairs (8 threads a token)
   const int rp = lora_pitch(a.rank), pitch = wide * 2 + 8;
   float* const sums = reinterpret_cast<float*>(shared_up);                       // [token][wide]
-  uint16_t* const pairs = reinterpret_cast<uint16_t*>(sums + kLoraTile * wide);
+  uint16_t* const pairs = reinterpret_cast<uint16_t*>(sums + kLoraTile * (wide + 8));
   {
     const int64_t step = (int64_t)a.plan.tokens * rp;
     for (int i = threadIdx.x; i < tile.count * (wide / 4); i += 64 * kLoraWaves) {
@@ -333,13 +339,13 @@ __global__ __launch_bounds__(64 * kLoraWaves, 4) void k_lora_up(LoraArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (r + j >= rank) s[j] = 0.0f;
-      *reinterpret_cast<v4f_t*>(sums + t * wide + r) = s;
+      *reinterpret_cast<v4f_t*>(sums + t * (wide + 8) + r) = s;
     }
   }
   __syncthreads();
   {
     const int t = threadIdx.x >> 3, sub = threadIdx.x & 7;
-    const float* const from = sums + t * wide;
+    const float* const from = sums + t * (wide + 8);
     const bool mine = t < tile.count;
     float top = 0.0f;
     for (int r = sub; r < wide; r += 8) {
@@ -414,7 +420,7 @@ __global__ __launch_bounds__(64 * kLoraWaves, 4) void k_lora_up(LoraArgs a) {
       }
     }
     if (chunk + 1 < chunks) return;
-    const int c = n_begin + (turn * kLoraWaves + wave) * 32 + 8 * part, left = n_end - c;
+    const int c = first + turn * 32 + 8 * part, left = n_end - c;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (!live[i] || left <= 0) continue;
@@ -436,32 +442,34 @@ __global__ __launch_bounds__(64 * kLoraWaves, 4) void k_lora_up(LoraArgs a) {
   }
 }
 
-// Over how many ranges K is split: four workgroups for every compute unit, each of 512 or more of K (a step of its eight
-// waves); more ranges are more to add up for every workgroup of the second kernel.
+// Over how many ranges K is split: two workgroups for every compute unit, each of 512 or more of K (a step of its eight
+// waves).  Every workgroup of the second kernel adds the ranges up: for four per compute unit 5003 tokens take 59 us, for
+// two 55, for one 56 and ranks of 128 81 instead of 70.
 struct LoraSplit {
   int splits, range;
 };
 static LoraSplit lora_split(int64_t tokens, int64_t K, int64_t rank, int64_t adapters) {
   const int64_t tiles = tokens / kLoraTile + std::min(tokens, adapters), groups = tiles * ((rank + 63) / 64);
-  int64_t s = (4 * (int64_t)num_cus() + groups - 1) / groups;
+  int64_t s = (2 * (int64_t)num_cus() + groups - 1) / groups;
   s = std::max<int64_t>(1, std::min<int64_t>({s, K / 512, kLoraSplits}));
   const int64_t range = round_up((K + s - 1) / s, 64);
   return {(int)((K + range - 1) / range), (int)range};
 }
 
 template <typename T>
-static int run_lora(const LoraArgs& a, int64_t most, hipStream_t stream) {
+static int run_lora(const LoraArgs& a, hipStream_t stream) {
   const char* what = "lora_add";
   const int rb = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
   const dim3 block(64 * kLoraWaves);
-  const dim3 down((unsigned)most, (unsigned)a.splits, (unsigned)((a.rank + 16 * rb - 1) / (16 * rb)));
+  const dim3 down((unsigned)(a.most * a.splits), (unsigned)((a.rank + 16 * rb - 1) / (16 * rb)));
   if (rb == 1) hipLaunchKernelGGL((k_lora_down<T, 1>), down, dim3(64 * kDownWaves), 0, stream, a);
   else if (rb == 2) hipLaunchKernelGGL((k_lora_down<T, 2>), down, dim3(64 * kDownWaves), 0, stream, a);
   else hipLaunchKernelGGL((k_lora_down<T, 4>), down, dim3(64 * kDownWaves), 0, stream, a);
   const int rc = check_launch(what);
   if (rc) return rc;
-  const dim3 up((unsigned)most, (unsigned)((a.N + kLoraChannels - 1) / kLoraChannels));
-  const size_t wide = lora_pitch(a.rank), lds = kLoraTile * (wide * 4 + (wide * 2 + 8) * 2);
+  const dim3 up((unsigned)((a.N + kLoraChannels - 1) / kLoraChannels), (unsigned)std::min(a.most, kLoraGridY),
+                (unsigned)((a.most + kLoraGridY - 1) / kLoraGridY));
+  const size_t wide = lora_pitch(a.rank), lds = kLoraTile * ((wide + 8) * 4 + (wide * 2 + 8) * 2);
   if (rb == 1) hipLaunchKernelGGL((k_lora_up<T, 1, 4>), up, block, lds, stream, a);
   else if (rb == 2) hipLaunchKernelGGL((k_lora_up<T, 2, 4>), up, block, lds, stream, a);
   else hipLaunchKernelGGL((k_lora_up<T, 4, 2>), up, block, lds, stream, a);
@@ -571,6 +579,6 @@ extern "C" int lora_add(const void* x, const void* a, const void* b, const float
   g.k_range = s.range;
   g.y = y;
   g.v = static_cast<float*>(workspace);
-  const int64_t most = lora_most_tiles(tokens, adapters);
-  return dt == FP8DP_BF16 ? run_lora<bf16_t>(g, most, stream) : run_lora<f16_t>(g, most, stream);
+  g.most = (int)lora_most_tiles(tokens, adapters);
+  return dt == FP8DP_BF16 ? run_lora<bf16_t>(g, stream) : run_lora<f16_t>(g, stream);
 }

@@ -149,6 +149,23 @@ def test_many_tokens():
     case(6000, 64, 64, 8, 300, F16)
 
 
+def test_more_tiles_than_a_grid_dimension():
+    tokens, N, K, rank = 32 * 32768 + 77, 8, 8, 3
+    x, a, b, scale = inputs(tokens, N, K, rank, 1, BF16)
+    base = draw((tokens, N), BF16, 5)
+    index = np.zeros(tokens, dtype=np.int64)
+    index[-60:] = -1
+    y = torch.full((tokens, N), float("nan"), dtype=BF16, device=DEV)
+    sq.lora_add(*(v.to(DEV) for v in (x, a, b, scale)), make_plan(index, 1), base.to(DEV), y,
+                workspace(tokens, N, K, rank, 1))
+    fx, fa, fb, fbase, fs = (v.double() for v in (x, a[0], b[0], base, scale[0]))
+    ref, size = fbase + fs * (fx @ fa.t()) @ fb.t(), fs * (fx.abs() @ fa.abs().t()) @ fb.abs().t()
+    ref[-60:], size[-60:] = fbase[-60:], 0.0
+    off = size * ((K / 16 + 64 + rank / 8 + 48) * 2 * U + half(BF16) ** 2) + 2 * U * (ref.abs() + fbase.abs())
+    assert ((y.cpu().double() - ref).abs() <= off + half(BF16) * (ref.abs() + off) + 2.0 ** -25).all()
+    assert torch.equal(y[-60:].cpu(), base[-60:])
+
+
 def test_one_plan_for_layers_of_other_sizes():
     tokens, adapters = 90, 4
     index = indexes("mixed", tokens, adapters, 2)

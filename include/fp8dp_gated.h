@@ -43,7 +43,7 @@ typedef enum {
    tiles of h, and copies operands whose rows K cuts to aligned ones; 0 where it would do neither. */
 int64_t gated_linear_workspace(int64_t M, int64_t N, int64_t K);
 
-/* The first half of a gated feed-forward layer, in one kernel:
+/* The first half of a gated feed-forward layer:
      g = x w_gate^T, u = x w_up^T, h = f(g) u, with f and the product on the binary32 sums.
    x: [M x K], w_gate, w_up: [N x K], h: [M x N], all of type dt, FP8DP_BF16 or FP8DP_F16.
    gate, up: [M x N] of type dt, g and u rounded, for the backward pass; both or neither.

@@ -31,7 +31,7 @@ def activation(g, act: str):
         return g * p, p + g * p * (1 - p) * 2 * c * (1 + 3 * 0.044715 * g * g)
     if act == "sigmoid":
         p = sigmoid(g)
-        return p, p * (1 - p)
+        return p, p * sigmoid(-g)
     if act == "relu":
         return np.maximum(g, 0), (g > 0).astype(np.float64)
     if act == "relu2":

@@ -35,7 +35,7 @@ __device__ __forceinline__ float gate_of(float g, float* slope) {
     }
     case FP8DP_GATE_SIGMOID: {
       const float p = sigmoid_of(g);
-      if (GRAD) *slope = p * (1.0f - p);
+      if (GRAD) *slope = p * sigmoid_of(-g);   // (1 - p would cancel: nothing was left of it from g = 17 on)
       return p;
     }
     case FP8DP_GATE_RELU:

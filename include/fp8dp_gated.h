@@ -62,7 +62,10 @@ int64_t gated_linear_backward_workspace(int64_t M, int64_t N, int64_t K);
 /* Backward of gated_linear from dh and the forward's x, gate and up:
      dg = dh u f'(g), du = dh f(g),
      dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x.
-   dg and du are rounded to dt, the matrix instructions' operand type; the sums are
+   dg and du are rounded to dt, the matrix instructions' operand type; in float16 they may be past that type's range:
+   where the largest finite magnitude of them all is outside [2^-6, 2^15), all are held times one power of two
+   that brings it to [2^14, 2^15) and that the outputs take back.  What float16 then holds as a subnormal is off by up to
+   2^-25, or 2^-39 of that largest magnitude where it was outside.  The sums are
    binary32 and have a fixed order: the same call gives the same bits.  All tensors are of
    type dt, dx [M x K], dw_gate and dw_up [N x K].  dx, or dw_gate and dw_up together, may be
    NULL and are then not computed.

@@ -83,7 +83,7 @@ int gated_linear_backward(const void* dh, const void* gate, const void* up, cons
      pre_rstd = 1 / sqrt(mean(z^2) + eps),  y = z * pre_rstd * pre_weight;
    the second norm reads z as stored.
    x NULL: the norm alone, of the residual as it is (z, post_weight, gate and post_rstd are
-   NULL then).  y NULL: no second norm.
+   NULL then).  y NULL: no second norm; pre_weight is not read then, and pre_rstd is NULL.
    post_weight, pre_weight: [cols] of type wt, dt or FP8DP_F32; NULL stands for ones.
    gate: NULL stands for ones; gate_per_token 0: [cols] of type gt, dt or FP8DP_F32; else
    [rows x cols] of type dt, and gt is dt.
@@ -91,7 +91,7 @@ int gated_linear_backward(const void* dh, const void* gate, const void* up, cons
    z may be x, residual or a gate per token.  A row that holds a NaN or an infinity gives NaN or 0
    where the formula does; other rows are not touched by it.
    Errors: EINVAL for a NULL residual, z without x or x without z, neither z nor y, what belongs to
-   an x that is NULL, rows or cols out of layer_norm's range, unknown types, a misaligned pointer, an eps that is
+   an x that is NULL, pre_rstd without y, rows or cols out of layer_norm's range, unknown types, a misaligned pointer, an eps that is
    negative or not finite, a scale that is not finite, or y the same buffer as z or an input. */
 int block_norm(const void* x, const void* residual, const void* post_weight, const void* gate,
                int32_t gate_per_token, const void* pre_weight, int64_t rows, int64_t cols,

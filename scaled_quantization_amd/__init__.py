@@ -898,7 +898,7 @@ def block_norm(x, residual: torch.Tensor, post_weight, gate, pre_weight, eps: fl
     """From one block to the next: z = residual_scale residual + branch_scale gate rms(x) post_weight
     and y = rms(z) pre_weight, rms(v) = v / sqrt(mean(v^2) + eps) over the last dimension.
     gate: [cols] (for an x of two dimensions or more), x's shape, or None; x None: y =
-    rms(residual) pre_weight; y None: z alone.  Weights of x's type or float32 (None: ones);
+    rms(residual) pre_weight; y None: z alone, without pre_rstd.  Weights of x's type or float32 (None: ones);
     post_rstd, pre_rstd: float32, one value per row, for the backward pass."""
     dt = _dtype(residual, "block_norm: residual")
     t, shape = residual.dtype, residual.shape

@@ -268,6 +268,10 @@ extern "C" int block_norm(const void* x, const void* residual, const void* post_
     set_error("%s: post_weight, gate and post_rstd belong to x", what);
     return FP8DP_EINVAL;
   }
+  if (y == nullptr && pre_rstd != nullptr) {
+    set_error("%s: pre_rstd belongs to y", what);
+    return FP8DP_EINVAL;
+  }
   const bool token = gate != nullptr && gate_per_token != 0;
   if ((rc = check_types(what, dt, wt)) || (rc = check_types(what, dt, gt))) return rc;
   if (token && gt != dt) {

@@ -92,7 +92,8 @@ int gated_linear_backward(const void* dh, const void* gate, const void* up, cons
    where the formula does; other rows are not touched by it.
    Errors: EINVAL for a NULL residual, z without x or x without z, neither z nor y, what belongs to
    an x that is NULL, pre_rstd without y, rows or cols out of layer_norm's range, unknown types, a misaligned pointer, an eps that is
-   negative or not finite, a scale that is not finite, or y the same buffer as z or an input. */
+   negative or not finite, a scale that is not finite, y or the statistics the same
+   buffer as z, an input or each other, or z the same as a weight, a gate per channel or a statistic. */
 int block_norm(const void* x, const void* residual, const void* post_weight, const void* gate,
                int32_t gate_per_token, const void* pre_weight, int64_t rows, int64_t cols,
                fp8dp_dtype dt, fp8dp_dtype wt, fp8dp_dtype gt, float residual_scale,
@@ -114,7 +115,8 @@ int block_norm(const void* x, const void* residual, const void* post_weight, con
    sums have a fixed order: the same call gives the same bits.
    dresidual may be dy or dz_add; dx and a dgate per token too where no other output is.
    Errors: EINVAL for a NULL dresidual, neither dy nor dz_add, neither dy nor x, an argument without what it belongs
-   to, outputs that are the same buffer or x, z or the gate, a missing workspace, and as above. */
+   to, outputs that are the same buffer or an input (but for those above) or the workspace, a missing workspace, and as
+   above. */
 int block_norm_backward(const void* dy, const void* dz_add, const void* x, const void* z,
                         const void* post_weight, const void* gate, int32_t gate_per_token,
                         const void* pre_weight, const float* post_rstd, const float* pre_rstd,

@@ -289,8 +289,9 @@ extern "C" int block_norm(const void* x, const void* residual, const void* post_
       !aligned_to(post_weight, we) || !aligned_to(pre_weight, we) ||
       !aligned_to(gate, dtype_size(gt)) || !aligned_to(post_rstd, 4) || !aligned_to(pre_rstd, 4))
     return bad_align(what);
-  if (y != nullptr && (y == z || y == x || y == residual || (token && y == gate))) {
-    set_error("%s: y must not be z, nor an input", what);
+  if (shared_buffers({y, post_rstd, pre_rstd}, {z, x, residual, gate, post_weight, pre_weight}) ||
+      shared_buffers({z}, {token ? nullptr : gate, post_weight, pre_weight})) {
+    set_error("%s: y and the statistics must not be z, an input or each other, nor z a parameter", what);
     return FP8DP_EINVAL;
   }
   BlockNormArgs a = {};

@@ -587,14 +587,14 @@ extern "C" int block_norm_backward(const void* dy, const void* dz_add, const voi
       !aligned_to(dx, e) || !aligned_to(dgate, token ? e : 4) || !aligned_to(dpost_weight, 4) ||
       !aligned_to(dpre_weight, 4) || !aligned_to(workspace, 4))
     return bad_align(what);
-  const void* const outs[] = {dresidual, dx, token ? dgate : nullptr};
-  for (int i = 0; i < 3; ++i)
-    for (int j = 0; j < 3; ++j)
-      if (outs[i] != nullptr && ((j != i && outs[i] == outs[j]) || outs[i] == x || outs[i] == z ||
-                                 (token && outs[i] == gate))) {
-        set_error("%s: dresidual, dx, dgate, x, z and gate must be different buffers", what);
-        return FP8DP_EINVAL;
-      }
+  const void* const gates = token ? nullptr : dgate;
+  if (shared_buffers({dresidual, dx, dgate, dpost_weight, dpre_weight},
+                     {x, z, gate, post_weight, pre_weight, post_rstd, pre_rstd, sums ? workspace : nullptr}) ||
+      shared_buffers({gates, dpost_weight, dpre_weight}, {dy, dz_add})) {
+    set_error("%s: gradients and inputs must be different buffers, but for dresidual, dx and a dgate per token in place of "
+              "dy or dz_add", what);
+    return FP8DP_EINVAL;
+  }
   BlockNormBwdArgs a = {};
   a.dy = dy;
   a.dz_add = dz_add;

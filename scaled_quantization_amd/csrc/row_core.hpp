@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 
 #include "codec.hpp"
 #include "common.hpp"
@@ -504,6 +505,17 @@ inline int check_types(const char* what, fp8dp_dtype dt, fp8dp_dtype wt) {
     return FP8DP_EINVAL;
   }
   return FP8DP_OK;
+}
+// Whether one of the outputs (NULL: not asked for) is another of them, or one of the inputs.
+inline bool shared_buffers(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+  for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
+    if (*o == nullptr) continue;
+    for (const void* const* p = outs.begin(); p != o; ++p)
+      if (*p == *o) return true;
+    for (const void* p : ins)
+      if (p == *o) return true;
+  }
+  return false;
 }
 inline int bad_align(const char* what) {
   set_error("%s: every pointer must be aligned to its elements", what);

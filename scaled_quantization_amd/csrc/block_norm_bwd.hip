@@ -149,9 +149,8 @@ __global__ __launch_bounds__(THR == 64 ? 64 * kBlockWaves : THR) void k_block_bw
     else earlier[(i * 16 + 8 + j) * THREADS] = __builtin_fmaf(x, y, earlier[(i * 16 + 8 + j) * THREADS]);
   };
 
-  // A cut vector is read as its row's last 8 elements, which another wave may write in place: of the
-  // first row all are read before any is written (of later rows the reductions' barriers see to it).
-  if constexpr (THR > 64) __syncthreads();
+  // (A cut vector is read as its row's last 8 elements, the first of which another wave may have written in place already: these
+  // are shifted out, so that no order is needed between the two.)
   int turn = 0;
   bool more = false;   // there are sums of earlier rows
   for (int64_t row = first;;) {

@@ -89,7 +89,9 @@ int gated_linear_backward(const void* dh, const void* gate, const void* up, cons
    [rows x cols] of type dt, and gt is dt.
    post_rstd, pre_rstd: [rows] floats that backward reads, or NULL.
    z may be x, residual or a gate per token.  A row that holds a NaN or an infinity gives NaN or 0
-   where the formula does; other rows are not touched by it.
+   where the formula does; other rows are not touched by it.  The squares are binary32 too: a row whose squares
+   add up to more than 3.4e38 has an inverse of 0, and one of values below 1e-19 counts as zeros (which shows with an eps of 0
+   alone).
    Errors: EINVAL for a NULL residual, z without x or x without z, neither z nor y, what belongs to
    an x that is NULL, pre_rstd without y, rows or cols out of layer_norm's range, unknown types, a misaligned pointer, an eps that is
    negative or not finite, a scale that is not finite, y or the statistics the same
@@ -151,7 +153,10 @@ int64_t lora_add_workspace(int64_t tokens, int64_t N, int64_t K, int64_t rank, i
    binary32 and multiplied by b_i as two 16-bit parts each, 16 bits of them in bfloat16 and 22 in float16.
    ranks: [adapters] 32-bit integers, of adapter i the first ranks[i] rows of a and columns of b count
    (what the others hold does not matter; below 0 is 0, above rank is rank), or NULL: all.
-   plan: lora_plan's for the same tokens and adapters.  base NULL: zeros.  y may be base.
+   plan: lora_plan's for the same tokens and adapters.  With one made for other numbers of them, or none, which only the
+   device can see, the call returns 0 and y stays as it is.  base NULL: zeros.  y may be base.
+   A token or a row of b that holds an infinity or a NaN gives infinities or NaN (NaN also where the formula has an
+   infinity: its parts are added), and no other token or channel is touched.
    workspace: 16-byte aligned, at least lora_add_workspace() bytes.
    Errors: EINVAL for a NULL x, a, b, scale, plan, y or workspace, tokens, adapters or rank out of range,
    N or K outside 1 .. FP8DP_GATED_MAX_WIDTH, another type, a misaligned pointer, or a workspace that is

@@ -868,7 +868,8 @@ def gated_linear_backward(dh: torch.Tensor, gate: torch.Tensor, up: torch.Tensor
                           w_gate: torch.Tensor, w_up: torch.Tensor, act: int, workspace: torch.Tensor,
                           dx=None, dw_gate=None, dw_up=None, stream=None) -> None:
     """Gradients of gated_linear from dh and the forward's gate and up: dx, and dw_gate with
-    dw_up, all of x's type.  workspace: at least gated_linear_backward_workspace(M, N, K) bytes."""
+    dw_up, all of x's type (in float16 also where the products in between leave its range).
+    workspace: at least gated_linear_backward_workspace(M, N, K) bytes."""
     name = "gated_linear_backward"
     M, N, K, dt = _gated(name, x, w_gate, w_up, (("dh", dh), ("gate", gate), ("up", up)))
     _like(dx, x.dtype, x.shape, f"{name}: dx")
@@ -993,7 +994,8 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: torch.Ten
              stream=None) -> None:
     """y [..., N] = base + scale[i] b[i] (a[i] x) for x [..., K], each token with the adapter i of
     the plan: a [adapters, rank, K], b [adapters, N, rank], bfloat16 or float16; scale float32, ranks
-    int32 (or None: all of rank), one per adapter.  base None: zeros; y may be base.  workspace: at
+    int32 (or None: all of rank), one per adapter.  base None: zeros; y may be base.  The plan must be one for
+    these numbers of tokens and adapters: with another y stays as it is.  workspace: at
     least lora_add_workspace(tokens, N, K, rank, adapters) bytes."""
     dt = _dtype(x, "lora_add: x")
     t, shape = x.dtype, x.shape

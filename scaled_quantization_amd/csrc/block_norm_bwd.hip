@@ -8,11 +8,15 @@
 //
 // With a gate per channel both of its sums are one: P = sum over rows of dz xh, dw_post = b gate P and
 // dgate = b w_post P; with one per token the sum is of gate dz xh.  So every form has two sums per column.
-// Rows of 8 to 8192 elements (of up to 16384 where there are not too many) are read once: a grid of resident workgroups walks the rows, each thread keeps the sums of its own columns, and
+// Rows of 8 to 8192 elements (of up to 16384 where there are at most 64 for each compute unit) are read once: a grid of resident workgroups walks the rows, each thread keeps the sums of its own columns, and
 // the workgroups' sums are added by a second kernel in a fixed order (no atomics: the same
 // call gives the same bits).  dz stays in registers between the row's two reductions.
 // Bound by memory with as many writes as reads nearly: 16384 x 4096 with a gate per token 205 us (5.2 TB/s), with one per
-// channel 155, 16384 x 768 37.
+// channel 155, 16384 x 768 36 (a quarter of the slots for vectors is empty).  Rows of 8193 to 16384 are bound by registers: the
+// compiler moves their parameters out of the loop over rows, and of the 128 registers a thread has it then spills up to 123
+// more (488 bytes a lane in bfloat16 with both norms and a gate per channel, 416 with one per token, 496 and 428 in float16,
+// 388 and 420 in binary32, whose 512-thread forms spill 44 and 200): 2048 x 16384 132 us for 60 of bytes.  What is left to
+// the kernel that reads a row again by each step is slow: 16384 x 12288 572 us, one row more 3290; 65536 x 7 2100.
 #include <hip/hip_runtime.h>
 
 #include "row_core.hpp"
@@ -503,7 +507,8 @@ static int launch_block_width(const BlockNormBwdArgs& a, BlockPartsArgs p, hipSt
     if (nvec <= 256) return launch_block_bwd<T, 1, 256, TOKEN, BRANCH, NORM>(a, p, stream);
     if (nvec <= 512) return launch_block_bwd<T, 2, 256, TOKEN, BRANCH, NORM>(a, p, stream);
     if (nvec <= 1024) return launch_block_bwd<T, 2, 512, TOKEN, BRANCH, NORM>(a, p, stream);
-    // sums of up to 64 rows each, one after another (2048 x 16384: 558 us by the kernel below)
+    // sums of up to 64 rows each, one after another, and no more: what they round off is not kept (2048 x 16384: 558 us by
+    // the kernel below)
     if (nvec <= 2048 && a.rows <= 64 * (int64_t)num_cus())
       return launch_block_bwd<T, 2, 1024, TOKEN, BRANCH, NORM>(a, p, stream);
   }

@@ -6,7 +6,8 @@
 //
 // Many tokens are bound by the matrix pipes and their power: 16384 x 8192 x 4096 takes 1540 us (1.43 PFLOP/s; a library's
 // product of the same size alone reaches 1.57) and 1650 where both projections are kept.  Few tokens are bound by the weights'
-// bytes: 48 x 16384 x 4096 58 us, 4.6 TB/s.  Small ones by launch, first copies and outputs: 777 x 1023 x 1001
+// bytes: 48 x 16384 x 4096 58 us, 4.6 TB/s (the tokens, brought in again for every 16 channels, are more bytes, from L2).  The
+// erf form of GELU is not hidden behind the products: 1750 for 1560.  Small ones by launch, first copies and outputs: 777 x 1023 x 1001
 // 18 us behind 4.6 for the aligned copies.
 #include "gated_core.hpp"
 #include "pad16.hpp"

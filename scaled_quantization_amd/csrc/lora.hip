@@ -3,7 +3,8 @@
 //   v[t] = a_i x[t],   y[t] = base[t] + scale_i b_i v[t],   i the adapter of token t
 //
 // A plan, made once per step, orders the tokens by adapter and cuts each adapter's into tiles of up to
-// 32, so that an adapter's weights are read once per tile.  Two kernels follow: the first gathers a
+// 32, so that an adapter's weights are read once per tile.  It takes one workgroup, whose waves hand out places to one adapter
+// of their 64 tokens a turn: 10 us for 64 tokens, 11 for 5003 of 8 adapters, 85 for 70000 in runs, 370 for 70000 mixed of 64.  Two kernels follow: the first gathers a
 // tile's tokens and leaves v in binary32, K split over workgroups where there are few tiles; the second adds
 // the ranges up and multiplies by b.  Each reads its weights once a tile; what bounds both is the way from the plan to the
 // data (entry, order, rows, weights: one waits for the other), so as many workgroups as fit are under way and each loads

@@ -23,7 +23,9 @@ inline int64_t tiles_of(TileShape t, int64_t m, int64_t n) {
 // compute unit to itself, 0.80 .. 0.85 for two, at any alignment 1.04 .. 1.30 and 1.35 .. 1.56.  A K that is
 // shared costs a join.  With estimates that favoured shares by a third more, gradients of 1025 x 1023 x 1001 took 50.5 us
 // for 45.9 (dx from three shares, now one), 8192 x 2048 x 768 169 for 161, one forward of 100 x 1024 x 1024 14.1 for 11.6;
-// 1000 x 8192 x 4096 is the worst loss that was found (302, now 312).
+// 1000 x 8192 x 4096 is the worst loss that was found (302, now 312).  256 x 192 was measured with operands that the caches
+// hold: dx of 16384 x 2048 x 768, whose [dg | du] comes from memory, takes 1.57 a stage.  There is no term for bytes, so that of
+// plans for few tokens and wide weights, which memory bounds, the estimates cannot tell the faster.
 inline ProductPlan plan_product(int64_t m, int64_t n, int64_t stages, bool dual, bool direct, double cus) {
   ProductPlan best = {direct ? kTile256 : kTileAny, 1};
   double least = 1e30;
